@@ -111,6 +111,9 @@ typedef struct {
  * takes precedence).  The call itself still runs, on whatever it was given.  The decode
  * step has no workspace to report into: it rejects this flag with M3_ERR_UNSUPPORTED. */
 #define M3_FLAG_DEBUG_CHECKS 8u
+/* The block operators (m3_conv_*, m3_sel_*) take these two and no other flag. */
+#define M3_FLAG_SILU 16u         /* m3_conv_*: the convolution's output goes through SiLU */
+#define M3_FLAG_DT_SOFTPLUS 32u  /* m3_sel_*: the step is softplus(dt + dt_bias) */
 
 /* Bytes of each state buffer for `dims`.  Any out-pointer may be NULL. */
 m3_status m3_state_bytes(const m3_dims* dims, size_t* h_bytes, size_t* x_prev_bytes,
@@ -409,6 +412,207 @@ m3_status m3_scan_bwd_ex(const m3_dims* dims, int32_t seqlen, const void* x, con
                          const m3_extras* extras, const void* dy, const float* dhT,
                          const m3_grads* grads, const m3_extra_grads* extra_grads,
                          void* workspace, size_t workspace_bytes, uint32_t flags, void* stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Block operators: what stands around a mixer in a layer.  A residual norm feeds the input
+ * projection; a short causal convolution and a selective scan with one decay per channel and
+ * state make the other mixer of hybrid stacks.  Prompts, single tokens and backward.
+ *
+ * Conventions, beside those at the top of this file
+ *   - Activations are m3_rows: [batch][T][width] tensors whose last axis is contiguous and
+ *     whose batch and token strides are the caller's (a half of a projection's output, a
+ *     transposed batch).  Input strides are >= 0 (0 reads one row again and again); output
+ *     rows must not overlap one another (M3_ERR_SHAPE).  Outputs must not overlap inputs
+ *     unless said so.  Any element alignment is accepted; rows that start on 16 bytes and are
+ *     a multiple of 16 bytes long take the wide loads.
+ *   - seqlens: device int32 [batch], or NULL for seqlen tokens in every sequence.  Sequence b
+ *     has min(max(seqlens[b], 0), seqlen) tokens; its later rows are read by nothing, and
+ *     y and the activation gradients are written as zeros there.  A sequence of length 0
+ *     leaves its state as it is.
+ *   - Unknown or foreign flags return M3_ERR_UNSUPPORTED.
+ *   - Sums and states are fp32; each output is rounded once to its type.  Every result is
+ *     the same from run to run (no atomics).
+ *   - Calls launch on the current device; `stream` must be a stream of it.
+ */
+typedef struct {
+    void* ptr;             /* device pointer to element (0, 0, 0), io dtype */
+    int64_t batch_stride;  /* in elements */
+    int64_t token_stride;  /* in elements; ignored by the single-token calls */
+} m3_rows;
+
+/*
+ * Short causal convolution over the tokens, one filter a channel:
+ *   pre_t[c] = bias[c] + sum_{k < W} weight[c][k] u_{t-W+1+k}[c],   y_t = pre_t or SiLU(pre_t),
+ * where u is the call's x with the state's W - 1 tokens before it.  The state is then the last
+ * W - 1 tokens of u, so calls chain: a prompt in pieces, then single tokens.
+ *   x, y    m3_rows [batch][T][channels] io dtype
+ *   weight  [channels][W] fp32, weight[c][W-1] is the current token's; bias [channels] fp32 or
+ *           NULL; both 4-byte aligned
+ *   state   [batch][W-1][channels] io dtype, packed, oldest token first, updated in place
+ *           (zeros start a sequence).  NULL is allowed for W = 1 alone.
+ * Width W is 1 to 8.  Flags: M3_FLAG_SILU.  seqlen 0 does nothing.
+ */
+typedef struct {
+    int32_t batch;
+    int32_t channels;
+    int32_t width;     /* W: taps, the current token's included */
+    int32_t io_dtype;  /* m3_dtype of x, y, state and the activation gradients */
+} m3_conv_dims;
+
+m3_status m3_conv_fwd(const m3_conv_dims* dims, int32_t seqlen, const m3_rows* x,
+                      const float* weight, const float* bias, const int32_t* seqlens,
+                      void* state, const m3_rows* y, uint32_t flags, void* stream);
+
+/* One token of every sequence: x and y are [batch][channels] (their token strides are ignored).
+ * y may be x itself (same pointer and batch stride). */
+m3_status m3_conv_step(const m3_conv_dims* dims, const m3_rows* x, const float* weight,
+                       const float* bias, void* state, const m3_rows* y, uint32_t flags,
+                       void* stream);
+
+/* Gradients of m3_conv_fwd given dL/dy.  state0 is the state that forward call started from
+ * (read only).  As with m3_scan_bwd, the carried state output gets no gradient here.
+ *   dx       m3_rows io dtype; dweight [channels][W], dbias [channels] (needed iff bias) and
+ *   dstate   [batch][W-1][channels] (gradient of state0; NULL: not wanted), fp32, overwritten.
+ * seqlen 0 writes zeros to dweight, dbias and dstate.
+ * Workspace (256-byte aligned): per-segment shares of dweight and dbias. */
+typedef struct {
+    m3_rows dx;
+    float* dweight;
+    float* dbias;
+    float* dstate;
+} m3_conv_grads;
+
+m3_status m3_conv_bwd_workspace_bytes(const m3_conv_dims* dims, int32_t seqlen, size_t* bytes);
+
+m3_status m3_conv_bwd(const m3_conv_dims* dims, int32_t seqlen, const m3_rows* x,
+                      const float* weight, const float* bias, const int32_t* seqlens,
+                      const void* state0, const m3_rows* dy, const m3_conv_grads* grads,
+                      void* workspace, size_t workspace_bytes, uint32_t flags, void* stream);
+
+/*
+ * Selective scan with a diagonal state per channel:
+ *   delta_t[c] = softplus(dt_t[c] + dt_bias[c])  (M3_FLAG_DT_SOFTPLUS; else dt_t[c] + dt_bias[c])
+ *   h_t[c][n]  = exp(delta_t[c] A[c][n]) h_{t-1}[c][n] + delta_t[c] x_t[c] B_t[g][n]
+ *   y_t[c]     = (sum_n C_t[g][n] h_t[c][n] + D[c] x_t[c]) * SiLU(z_t[c])
+ * Channel c reads group g = c / (channels / ngroups).  The mixer's recurrence (m3_scan_fwd) has
+ * one decay per head and token; this one has its own decay in every channel and state.
+ *   x, dt, z, y   m3_rows [batch][T][channels] io dtype; z.ptr NULL: no gate
+ *   B, C          m3_rows [batch][T][ngroups * dstate] io dtype
+ *   A             [channels][dstate] fp32; D, dt_bias [channels] fp32 or NULL
+ *   h             [batch][channels][dstate] fp32, updated in place (4-byte aligned)
+ * dstate 1 to 256; ngroups divides channels.  The caller's contract is delta >= 0 and A <= 0
+ * (a growing state is computed as it stands and may overflow).  seqlen 0 does nothing.
+ * Flags: M3_FLAG_DT_SOFTPLUS.
+ * Workspace: m3_sel_workspace_bytes, 256-byte aligned.  Long sequences with too few channels to
+ * fill the GPU are split into segments run side by side; the workspace holds each segment's
+ * state.  With less room, or NULL, the call runs unsegmented, the same up to rounding.
+ */
+typedef struct {
+    int32_t batch;
+    int32_t channels;
+    int32_t ngroups;
+    int32_t dstate;
+    int32_t io_dtype;  /* m3_dtype of x, dt, B, C, z, y and the activation gradients */
+} m3_sel_dims;
+
+typedef struct {
+    m3_rows x;
+    m3_rows dt;
+    m3_rows B;
+    m3_rows C;
+    m3_rows z;
+    const float* A;
+    const float* D;
+    const float* dt_bias;
+    const int32_t* seqlens;  /* m3_sel_step: must be NULL */
+} m3_sel_inputs;
+
+m3_status m3_sel_workspace_bytes(const m3_sel_dims* dims, int32_t seqlen, size_t* bytes);
+
+m3_status m3_sel_fwd(const m3_sel_dims* dims, int32_t seqlen, const m3_sel_inputs* in, float* h,
+                     const m3_rows* y, void* workspace, size_t workspace_bytes, uint32_t flags,
+                     void* stream);
+
+/* One token of every sequence (token strides are ignored): one pass over the state.  y may be
+ * x or z itself (same pointer and batch stride). */
+m3_status m3_sel_step(const m3_sel_dims* dims, const m3_sel_inputs* in, float* h,
+                      const m3_rows* y, uint32_t flags, void* stream);
+
+/* Gradients of m3_sel_fwd given dL/dy and, optionally, dL/dh_T.  h0 is the state that forward
+ * call started from (read only), dhT [batch][channels][dstate] fp32 or NULL (zero).
+ *   dx, ddt, dz   m3_rows [batch][T][channels] io dtype (dz needed iff z)
+ *   dB, dC        m3_rows [batch][T][ngroups * dstate] io dtype, summed over the group
+ *   dA [channels][dstate], dD (needed iff D), ddt_bias (needed iff dt_bias) [channels] and
+ *   dh [batch][channels][dstate] (gradient of h0; NULL: not wanted), fp32, overwritten.
+ * seqlen 0 writes dh = dhT and zeros to dA, dD and ddt_bias.
+ * Workspace: m3_sel_bwd_workspace_bytes, 256-byte aligned. */
+typedef struct {
+    m3_rows dx;
+    m3_rows ddt;
+    m3_rows dB;
+    m3_rows dC;
+    m3_rows dz;
+    float* dA;
+    float* dD;
+    float* ddt_bias;
+    float* dh;
+} m3_sel_grads;
+
+m3_status m3_sel_bwd_workspace_bytes(const m3_sel_dims* dims, int32_t seqlen, size_t* bytes);
+
+m3_status m3_sel_bwd(const m3_sel_dims* dims, int32_t seqlen, const m3_sel_inputs* in,
+                     const float* h0, const m3_rows* dy, const float* dhT,
+                     const m3_sel_grads* grads, void* workspace, size_t workspace_bytes,
+                     uint32_t flags, void* stream);
+
+/*
+ * RMS norm with the residual's addition:
+ *   r = x + residual, rounded to res_dtype and kept in residual_out;
+ *   y = r / sqrt(mean_i r_i^2 + eps) * weight       (of the rounded r)
+ *   x        [rows][width] io dtype, row stride x_stride
+ *   residual [rows][width] res_dtype or NULL (r = x, unrounded; res_dtype is then that of x)
+ *   residual_out [rows][width] res_dtype or NULL (not kept); may be the residual itself, or with
+ *            no residual x itself (same pointer and stride)
+ *   weight   [width] fp32 or NULL (ones)
+ *   y        M3_OUT_IO: [rows][width] io dtype; may be x itself (same pointer and stride).
+ *            M3_OUT_E4M3: [rows][width] e4m3 bytes, q = round(y / scale) with one fp32 scale for
+ *            each 128 consecutive values of a row (the last group may be shorter),
+ *            scale = max(max |y|, 2^-100) / 448, in scales [rows][ceil(width / 128)], packed.
+ *            y stands for q * scale.  A group that holds a NaN or an infinity has a NaN scale.
+ * Strides are in elements and at least width.  width is at most 32768.  eps >= 0
+ * (M3_ERR_SHAPE otherwise).  rows 0 does nothing.  No workspace.
+ */
+typedef enum { M3_OUT_IO = 0, M3_OUT_E4M3 = 1 } m3_norm_out;
+
+typedef struct {
+    int32_t rows;
+    int32_t width;
+    int32_t io_dtype;   /* m3_dtype of x, of y with M3_OUT_IO, of dy and dx */
+    int32_t res_dtype;  /* m3_dtype of the residual; io_dtype where there is none */
+    int32_t out;        /* m3_norm_out (m3_norm_fwd alone reads it) */
+} m3_norm_dims;
+
+m3_status m3_norm_fwd(const m3_norm_dims* dims, const void* x, int64_t x_stride,
+                      const void* residual, int64_t residual_stride, const float* weight,
+                      float eps, void* y, int64_t y_stride, float* scales, void* residual_out,
+                      int64_t residual_out_stride, void* stream);
+
+/* Gradients of m3_norm_fwd:  with u = r / sqrt(mean r^2 + eps),
+ *   dr = (dy w - u mean_i(dy w u)) / sqrt(mean r^2 + eps) + dres,   dweight = sum_rows dy u.
+ *   r        [rows][width] res_dtype: the residual_out of the forward call (x without residual)
+ *   dy       [rows][width] io dtype (with M3_OUT_E4M3: the gradient of the unquantised y)
+ *   dres     [rows][width] res_dtype: gradient of residual_out, or NULL (zero)
+ *   dx       [rows][width] io dtype: dr; may be dy itself (same pointer and stride)
+ *   dresidual [rows][width] res_dtype: dr, or NULL; may be dres itself (same pointer and stride)
+ *   dweight  [width] fp32, overwritten; needed iff weight
+ * rows 0 writes zeros to dweight.  Workspace (256-byte aligned): per-block shares of dweight. */
+m3_status m3_norm_bwd_workspace_bytes(const m3_norm_dims* dims, size_t* bytes);
+
+m3_status m3_norm_bwd(const m3_norm_dims* dims, const void* r, int64_t r_stride,
+                      const float* weight, float eps, const void* dy, int64_t dy_stride,
+                      const void* dres, int64_t dres_stride, void* dx, int64_t dx_stride,
+                      void* dresidual, int64_t dresidual_stride, float* dweight, void* workspace,
+                      size_t workspace_bytes, void* stream);
 
 /* Synchronise `stream` and report the device-side status word in `workspace`:
  * M3_OK, M3_ERR_TIMEOUT when a bounded wait gave up, or M3_ERR_RANGE when the debug

@@ -1,0 +1,503 @@
+// block_api.cu -- C ABI of the block operators (m3_conv_*, m3_sel_*, m3_norm_*): host-side
+// validation and dispatch.  Everything is checked before anything is launched.
+#include <cmath>
+#include <cstring>
+
+#include "block_internal.h"
+
+using namespace m3;
+
+namespace {
+
+bool at_least(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+size_t esize(int io) { return io == M3_BF16 ? 2 : 4; }
+bool io_known(int io) { return io == M3_F32 || io == M3_BF16; }
+
+m3_status status_of(cudaError_t e) {
+    if (e == cudaSuccess) return M3_OK;
+    return e == cudaErrorNotSupported ? M3_ERR_UNSUPPORTED : M3_ERR_LAUNCH;
+}
+
+// Geometry of one call's rows.  step: one token a sequence (token strides unused).
+struct Geo {
+    int64_t batch, T;
+    size_t e;
+    bool step;
+};
+
+m3_status check_in(const m3_rows& r, const Geo& g) {
+    if (!r.ptr) return M3_ERR_NULL;
+    if (!at_least(r.ptr, g.e)) return M3_ERR_ALIGN;
+    if (r.batch_stride < 0 || (!g.step && r.token_stride < 0)) return M3_ERR_SHAPE;
+    return M3_OK;
+}
+
+// Output rows must not overlap: one of the two axes lies inside the other.
+m3_status check_out(const m3_rows& r, const Geo& g, int64_t width) {
+    m3_status st = check_in(r, g);
+    if (st != M3_OK) return st;
+    const int64_t T = g.step ? 1 : g.T, bs = r.batch_stride, ts = r.token_stride;
+    if (T > 1 && ts < width) return M3_ERR_SHAPE;
+    if (g.batch > 1 && bs < width) return M3_ERR_SHAPE;
+    if (T > 1 && g.batch > 1) {
+        // span / stride compared by division: no product of strides and counts can overflow
+        const bool tokens_inside = (bs - width) / ts >= T - 1;
+        const bool batch_inside = (ts - width) / bs >= g.batch - 1;
+        if (!tokens_inside && !batch_inside) return M3_ERR_SHAPE;
+    }
+    return M3_OK;
+}
+
+// Whether every row starts on 16 bytes.
+bool wide_rows(const m3_rows& r, const Geo& g) {
+    const int64_t per = 16 / (int64_t)g.e;
+    return at_least(r.ptr, 16) && (g.batch == 1 || r.batch_stride % per == 0) &&
+           (g.step || g.T == 1 || r.token_stride % per == 0);
+}
+
+View view(const m3_rows& r) { return View{r.ptr, r.batch_stride, r.token_stride}; }
+template <typename O>
+void set_out(O& o, const m3_rows& r) {
+    o.p = r.ptr;
+    o.bs = r.batch_stride;
+    o.ts = r.token_stride;
+}
+
+constexpr int64_t kMaxBlocks = 2147483647;   // a one-dimensional grid
+
+// ------------------------------------------------------------------ convolution
+
+m3_status conv_dims_ok(const m3_conv_dims* d) {
+    if (!d) return M3_ERR_NULL;
+    if (!io_known(d->io_dtype)) return M3_ERR_DTYPE;
+    if (d->batch < 1 || d->channels < 1 || d->width < 1) return M3_ERR_SHAPE;
+    if (d->width > 8 || d->channels > 1 << 24) return M3_ERR_UNSUPPORTED;
+    return M3_OK;
+}
+
+// Tokens of a run: long enough that the W - 1 tokens read again at its start cost little, short
+// enough that small calls still spread over the GPU (about four blocks an SM).
+void conv_runs(const m3_conv_dims* d, int32_t T, int most, int* seg, int* nseg) {
+    const int V = 16 / (int)esize(d->io_dtype);
+    const int64_t blocks = (int64_t)d->batch * ((d->channels + 128 * V - 1) / (128 * V));
+    int s = most;
+    while (s > 8 && blocks * ((T + s - 1) / s) < 148 * 4) s /= 2;
+    *seg = s;
+    *nseg = (T + s - 1) / s;
+}
+
+m3_status conv_common(const m3_conv_dims* d, const Geo& g, const m3_rows* x, const float* weight,
+                      const float* bias, const int32_t* seqlens, const void* state, uint32_t flags) {
+    if (flags & ~M3_FLAG_SILU) return M3_ERR_UNSUPPORTED;
+    if (!x || !weight || (d->width > 1 && !state)) return M3_ERR_NULL;
+    m3_status st = check_in(*x, g);
+    if (st != M3_OK) return st;
+    if (!at_least(weight, 4) || (bias && !at_least(bias, 4)) || (seqlens && !at_least(seqlens, 4)) ||
+        !at_least(state, g.e))
+        return M3_ERR_ALIGN;
+    return M3_OK;
+}
+
+void conv_args(ConvArgs* a, const m3_conv_dims* d, int32_t T, const m3_rows* x, const float* weight,
+               const float* bias, const int32_t* seqlens, const void* state, uint32_t flags) {
+    std::memset(a, 0, sizeof(*a));
+    a->x = view(*x);
+    a->weight = weight;
+    a->bias = bias;
+    a->seqlens = seqlens;
+    a->state = const_cast<void*>(state);
+    a->batch = d->batch;
+    a->T = T;
+    a->C = d->channels;
+    a->W = d->width;
+    a->silu = flags & M3_FLAG_SILU;
+}
+
+bool conv_wide(const m3_conv_dims* d, const void* state) {
+    return d->channels % (16 / (int)esize(d->io_dtype)) == 0 && at_least(state, 16);
+}
+
+}  // namespace
+
+extern "C" {
+
+m3_status m3_conv_fwd(const m3_conv_dims* d, int32_t T, const m3_rows* x, const float* weight,
+                      const float* bias, const int32_t* seqlens, void* state, const m3_rows* y,
+                      uint32_t flags, void* stream) {
+    m3_status st = conv_dims_ok(d);
+    if (st != M3_OK) return st;
+    if (T < 0) return M3_ERR_SHAPE;
+    if (flags & ~M3_FLAG_SILU) return M3_ERR_UNSUPPORTED;
+    if (T == 0) return M3_OK;
+    const Geo g{d->batch, T, esize(d->io_dtype), false};
+    if ((st = conv_common(d, g, x, weight, bias, seqlens, state, flags)) != M3_OK) return st;
+    if (!y) return M3_ERR_NULL;
+    if ((st = check_out(*y, g, d->channels)) != M3_OK) return st;
+    ConvArgs a;
+    conv_args(&a, d, T, x, weight, bias, seqlens, state, flags);
+    set_out(a.y, *y);
+    conv_runs(d, T, 64, &a.seg, &a.nseg);
+    if ((int64_t)a.batch * a.nseg > kMaxBlocks) return M3_ERR_UNSUPPORTED;
+    a.wide = conv_wide(d, state) && wide_rows(*x, g) && wide_rows(*y, g);
+    return status_of(launch_conv(a, ConvCall::fwd, d->io_dtype, static_cast<cudaStream_t>(stream)));
+}
+
+m3_status m3_conv_step(const m3_conv_dims* d, const m3_rows* x, const float* weight,
+                       const float* bias, void* state, const m3_rows* y, uint32_t flags,
+                       void* stream) {
+    m3_status st = conv_dims_ok(d);
+    if (st != M3_OK) return st;
+    const Geo g{d->batch, 1, esize(d->io_dtype), true};
+    if ((st = conv_common(d, g, x, weight, bias, nullptr, state, flags)) != M3_OK) return st;
+    if (!y) return M3_ERR_NULL;
+    if ((st = check_out(*y, g, d->channels)) != M3_OK) return st;
+    if ((int64_t)d->batch * d->channels / 128 + 1 > kMaxBlocks) return M3_ERR_UNSUPPORTED;
+    ConvArgs a;
+    conv_args(&a, d, 1, x, weight, bias, nullptr, state, flags);
+    set_out(a.y, *y);
+    a.wide = conv_wide(d, state) && wide_rows(*x, g) && wide_rows(*y, g);
+    return status_of(launch_conv(a, ConvCall::step, d->io_dtype, static_cast<cudaStream_t>(stream)));
+}
+
+m3_status m3_conv_bwd_workspace_bytes(const m3_conv_dims* d, int32_t T, size_t* bytes) {
+    m3_status st = conv_dims_ok(d);
+    if (st != M3_OK) return st;
+    if (!bytes) return M3_ERR_NULL;
+    if (T < 0) return M3_ERR_SHAPE;
+    int seg, nseg;
+    conv_runs(d, T, 128, &seg, &nseg);
+    const size_t n = sizeof(float) * (size_t)d->batch * nseg * (d->width + 1) * d->channels;
+    *bytes = n < 256 ? 256 : (n + 255) / 256 * 256;
+    return M3_OK;
+}
+
+m3_status m3_conv_bwd(const m3_conv_dims* d, int32_t T, const m3_rows* x, const float* weight,
+                      const float* bias, const int32_t* seqlens, const void* state0,
+                      const m3_rows* dy, const m3_conv_grads* gr, void* ws, size_t ws_bytes,
+                      uint32_t flags, void* stream) {
+    m3_status st = conv_dims_ok(d);
+    if (st != M3_OK) return st;
+    if (T < 0) return M3_ERR_SHAPE;
+    if (flags & ~M3_FLAG_SILU) return M3_ERR_UNSUPPORTED;
+    if (!gr || !gr->dweight || (bias && !gr->dbias)) return M3_ERR_NULL;
+    if (!at_least(gr->dweight, 4) || (gr->dbias && !at_least(gr->dbias, 4)) ||
+        (gr->dstate && !at_least(gr->dstate, 4)))
+        return M3_ERR_ALIGN;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const size_t C = d->channels, W = d->width;
+    if (T == 0) {
+        cudaError_t e = cudaMemsetAsync(gr->dweight, 0, C * W * sizeof(float), s);
+        if (e == cudaSuccess && bias) e = cudaMemsetAsync(gr->dbias, 0, C * sizeof(float), s);
+        if (e == cudaSuccess && gr->dstate && W > 1)
+            e = cudaMemsetAsync(gr->dstate, 0, (size_t)d->batch * (W - 1) * C * sizeof(float), s);
+        return e == cudaSuccess ? M3_OK : M3_ERR_CUDA;
+    }
+    const Geo g{d->batch, T, esize(d->io_dtype), false};
+    if ((st = conv_common(d, g, x, weight, bias, seqlens, state0, flags)) != M3_OK) return st;
+    if (!dy) return M3_ERR_NULL;
+    if ((st = check_in(*dy, g)) != M3_OK) return st;
+    if ((st = check_out(gr->dx, g, d->channels)) != M3_OK) return st;
+    size_t need;
+    m3_conv_bwd_workspace_bytes(d, T, &need);
+    if (!ws || !at_least(ws, 256) || ws_bytes < need) return M3_ERR_WORKSPACE;
+    ConvArgs a;
+    conv_args(&a, d, T, x, weight, bias, seqlens, state0, flags);
+    a.dy = view(*dy);
+    set_out(a.dx, gr->dx);
+    a.dweight = gr->dweight;
+    a.dbias = bias ? gr->dbias : nullptr;
+    a.dstate = gr->dstate;
+    a.part = static_cast<float*>(ws);
+    conv_runs(d, T, 128, &a.seg, &a.nseg);
+    if ((int64_t)a.batch * a.nseg > kMaxBlocks) return M3_ERR_UNSUPPORTED;
+    a.wide = conv_wide(d, state0) && wide_rows(*x, g) && wide_rows(*dy, g) && wide_rows(gr->dx, g);
+    return status_of(launch_conv(a, ConvCall::bwd, d->io_dtype, s));
+}
+
+}  // extern "C"
+
+namespace {
+
+// ------------------------------------------------------------------ selective scan
+
+m3_status sel_dims_ok(const m3_sel_dims* d) {
+    if (!d) return M3_ERR_NULL;
+    if (!io_known(d->io_dtype)) return M3_ERR_DTYPE;
+    if (d->batch < 1 || d->channels < 1 || d->ngroups < 1 || d->dstate < 1) return M3_ERR_SHAPE;
+    if (d->channels % d->ngroups) return M3_ERR_SHAPE;
+    if (d->dstate > 256 || d->channels > 1 << 24) return M3_ERR_UNSUPPORTED;
+    return M3_OK;
+}
+
+m3_status sel_common(const m3_sel_dims* d, const Geo& g, const m3_sel_inputs* in, const void* h) {
+    if (!in || !in->A || !h) return M3_ERR_NULL;
+    m3_status st;
+    for (const m3_rows* r : {&in->x, &in->dt, &in->B, &in->C})
+        if ((st = check_in(*r, g)) != M3_OK) return st;
+    if (in->z.ptr && (st = check_in(in->z, g)) != M3_OK) return st;
+    if (!at_least(in->A, 4) || !at_least(h, 4) || (in->D && !at_least(in->D, 4)) ||
+        (in->dt_bias && !at_least(in->dt_bias, 4)) || (in->seqlens && !at_least(in->seqlens, 4)))
+        return M3_ERR_ALIGN;
+    return M3_OK;
+}
+
+void sel_args(SelArgs* a, const m3_sel_dims* d, int32_t T, const m3_sel_inputs* in, const float* h,
+              uint32_t flags) {
+    std::memset(a, 0, sizeof(*a));
+    a->x = view(in->x);
+    a->dt = view(in->dt);
+    a->B = view(in->B);
+    a->C = view(in->C);
+    a->z = view(in->z);
+    a->A = in->A;
+    a->Dskip = in->D;
+    a->dt_bias = in->dt_bias;
+    a->seqlens = in->seqlens;
+    a->h = const_cast<float*>(h);
+    a->batch = d->batch;
+    a->T = T;
+    a->D = d->channels;
+    a->G = d->ngroups;
+    a->N = d->dstate;
+    a->softplus = flags & M3_FLAG_DT_SOFTPLUS;
+}
+
+// An upper bound of the blocks of any launch over (tile, segment, batch) or over the states.
+bool sel_grid_ok(const SelArgs& a) {
+    const double cells = (double)a.batch * a.D * a.nseg;
+    const double rows = (double)a.batch * a.T * a.G * 2 * a.N;
+    return cells < 2147483647.0 && rows / 256 < 2147483646.0 &&
+           (double)a.batch * a.D * a.N / 128 < 2147483646.0;
+}
+
+}  // namespace
+
+extern "C" {
+
+m3_status m3_sel_workspace_bytes(const m3_sel_dims* d, int32_t T, size_t* bytes) {
+    m3_status st = sel_dims_ok(d);
+    if (st != M3_OK) return st;
+    if (!bytes) return M3_ERR_NULL;
+    if (T < 0) return M3_ERR_SHAPE;
+    const size_t n = T ? sel_fwd_workspace(d->batch, T, d->channels, d->ngroups, d->dstate) : 0;
+    *bytes = n < 256 ? 256 : (n + 255) / 256 * 256;
+    return M3_OK;
+}
+
+m3_status m3_sel_fwd(const m3_sel_dims* d, int32_t T, const m3_sel_inputs* in, float* h,
+                     const m3_rows* y, void* ws, size_t ws_bytes, uint32_t flags, void* stream) {
+    m3_status st = sel_dims_ok(d);
+    if (st != M3_OK) return st;
+    if (T < 0) return M3_ERR_SHAPE;
+    if (flags & ~M3_FLAG_DT_SOFTPLUS) return M3_ERR_UNSUPPORTED;
+    if (ws && !at_least(ws, 256)) return M3_ERR_WORKSPACE;
+    if (T == 0) return M3_OK;
+    const Geo g{d->batch, T, esize(d->io_dtype), false};
+    if ((st = sel_common(d, g, in, h)) != M3_OK) return st;
+    if (!y) return M3_ERR_NULL;
+    if ((st = check_out(*y, g, d->channels)) != M3_OK) return st;
+    SelArgs a;
+    sel_args(&a, d, T, in, h, flags);
+    set_out(a.y, *y);
+    a.nseg = sel_fwd_segments(a.batch, T, a.D, a.G, a.N, &a.seg);
+    if (a.nseg > 1 && (!ws || ws_bytes < sel_fwd_workspace(a.batch, T, a.D, a.G, a.N))) a.nseg = 1;
+    if (a.nseg == 1) a.seg = T;
+    a.hseg = static_cast<float*>(ws);
+    a.dsum = a.hseg + (size_t)a.batch * a.nseg * a.D * a.N;
+    if (!sel_grid_ok(a)) return M3_ERR_UNSUPPORTED;
+    return status_of(launch_sel_fwd(a, d->io_dtype, static_cast<cudaStream_t>(stream)));
+}
+
+m3_status m3_sel_step(const m3_sel_dims* d, const m3_sel_inputs* in, float* h, const m3_rows* y,
+                      uint32_t flags, void* stream) {
+    m3_status st = sel_dims_ok(d);
+    if (st != M3_OK) return st;
+    if (flags & ~M3_FLAG_DT_SOFTPLUS) return M3_ERR_UNSUPPORTED;
+    const Geo g{d->batch, 1, esize(d->io_dtype), true};
+    if ((st = sel_common(d, g, in, h)) != M3_OK) return st;
+    if (in->seqlens) return M3_ERR_UNSUPPORTED;
+    if (!y) return M3_ERR_NULL;
+    if ((st = check_out(*y, g, d->channels)) != M3_OK) return st;
+    SelArgs a;
+    sel_args(&a, d, 1, in, h, flags);
+    set_out(a.y, *y);
+    a.nseg = 1;
+    if ((double)a.batch * a.D / 16 > 2147483646.0) return M3_ERR_UNSUPPORTED;
+    a.wide = a.N % 4 == 0 && at_least(h, 16) && at_least(in->A, 16);
+    return status_of(launch_sel_step(a, d->io_dtype, static_cast<cudaStream_t>(stream)));
+}
+
+m3_status m3_sel_bwd_workspace_bytes(const m3_sel_dims* d, int32_t T, size_t* bytes) {
+    m3_status st = sel_dims_ok(d);
+    if (st != M3_OK) return st;
+    if (!bytes) return M3_ERR_NULL;
+    if (T < 0) return M3_ERR_SHAPE;
+    SelArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.batch = d->batch; a.T = T; a.D = d->channels; a.G = d->ngroups; a.N = d->dstate;
+    const size_t n = sel_bwd_plan(&a, d->io_dtype, nullptr);
+    *bytes = n < 256 ? 256 : n;
+    return M3_OK;
+}
+
+m3_status m3_sel_bwd(const m3_sel_dims* d, int32_t T, const m3_sel_inputs* in, const float* h0,
+                     const m3_rows* dy, const float* dhT, const m3_sel_grads* gr, void* ws,
+                     size_t ws_bytes, uint32_t flags, void* stream) {
+    m3_status st = sel_dims_ok(d);
+    if (st != M3_OK) return st;
+    if (T < 0) return M3_ERR_SHAPE;
+    if (flags & ~M3_FLAG_DT_SOFTPLUS) return M3_ERR_UNSUPPORTED;
+    if (!in || !gr || !gr->dA || (in->D && !gr->dD) || (in->dt_bias && !gr->ddt_bias))
+        return M3_ERR_NULL;
+    for (const float* f : {dhT, (const float*)gr->dA, (const float*)gr->dD,
+                           (const float*)gr->ddt_bias, (const float*)gr->dh})
+        if (f && !at_least(f, 4)) return M3_ERR_ALIGN;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const size_t D = d->channels, N = d->dstate, hb = sizeof(float) * (size_t)d->batch * D * N;
+    if (T == 0) {
+        cudaError_t e = cudaMemsetAsync(gr->dA, 0, D * N * sizeof(float), s);
+        if (e == cudaSuccess && in->D) e = cudaMemsetAsync(gr->dD, 0, D * sizeof(float), s);
+        if (e == cudaSuccess && in->dt_bias)
+            e = cudaMemsetAsync(gr->ddt_bias, 0, D * sizeof(float), s);
+        if (e == cudaSuccess && gr->dh && gr->dh != dhT)
+            e = dhT ? cudaMemcpyAsync(gr->dh, dhT, hb, cudaMemcpyDeviceToDevice, s)
+                    : cudaMemsetAsync(gr->dh, 0, hb, s);
+        return e == cudaSuccess ? M3_OK : M3_ERR_CUDA;
+    }
+    const Geo g{d->batch, T, esize(d->io_dtype), false};
+    if ((st = sel_common(d, g, in, h0)) != M3_OK) return st;
+    if (!dy) return M3_ERR_NULL;
+    if ((st = check_in(*dy, g)) != M3_OK) return st;
+    const int64_t bn = (int64_t)d->ngroups * d->dstate;
+    if ((st = check_out(gr->dx, g, d->channels)) != M3_OK ||
+        (st = check_out(gr->ddt, g, d->channels)) != M3_OK ||
+        (st = check_out(gr->dB, g, bn)) != M3_OK || (st = check_out(gr->dC, g, bn)) != M3_OK ||
+        (in->z.ptr && (st = check_out(gr->dz, g, d->channels)) != M3_OK))
+        return st;
+    SelArgs a;
+    sel_args(&a, d, T, in, h0, flags);
+    const size_t need = sel_bwd_plan(&a, d->io_dtype, static_cast<char*>(ws));
+    if (!ws || !at_least(ws, 256) || ws_bytes < need) return M3_ERR_WORKSPACE;
+    if (!sel_grid_ok(a)) return M3_ERR_UNSUPPORTED;
+    a.dy = view(*dy);
+    set_out(a.dx, gr->dx);
+    set_out(a.ddt, gr->ddt);
+    set_out(a.dB, gr->dB);
+    set_out(a.dC, gr->dC);
+    set_out(a.dz, gr->dz);
+    a.dhT = dhT;
+    a.dA = gr->dA;
+    a.dD = in->D ? gr->dD : nullptr;
+    a.ddt_bias = in->dt_bias ? gr->ddt_bias : nullptr;
+    a.dh = gr->dh;
+    return status_of(launch_sel_bwd(a, d->io_dtype, s));
+}
+
+}  // extern "C"
+
+namespace {
+
+// ------------------------------------------------------------------ norm
+
+m3_status norm_dims_ok(const m3_norm_dims* d) {
+    if (!d) return M3_ERR_NULL;
+    if (!io_known(d->io_dtype) || !io_known(d->res_dtype)) return M3_ERR_DTYPE;
+    if (d->out != M3_OUT_IO && d->out != M3_OUT_E4M3) return M3_ERR_DTYPE;
+    if (d->rows < 0 || d->width < 1) return M3_ERR_SHAPE;
+    if (d->width > 32768) return M3_ERR_UNSUPPORTED;
+    return M3_OK;
+}
+
+// A [rows][width] tensor of e-byte elements, or an absent optional one (ok).
+m3_status check_mat(const void* p, int64_t stride, const m3_norm_dims* d, size_t e, bool needed) {
+    if (!p) return needed ? M3_ERR_NULL : M3_OK;
+    if (!at_least(p, e)) return M3_ERR_ALIGN;
+    if (d->rows > 1 && stride < d->width) return M3_ERR_SHAPE;
+    return M3_OK;
+}
+
+// Rows of vectors of 8 values: 16-byte aligned (e4m3: 8 bytes).
+bool wide_mat(const void* p, int64_t stride, const m3_norm_dims* d, size_t e) {
+    const size_t a = e == 1 ? 8 : 16;
+    return !p || (at_least(p, a) && (d->rows == 1 || stride * (int64_t)e % (int64_t)a == 0));
+}
+
+}  // namespace
+
+extern "C" {
+
+m3_status m3_norm_fwd(const m3_norm_dims* d, const void* x, int64_t xs, const void* res, int64_t rs,
+                      const float* weight, float eps, void* y, int64_t ys, float* scales,
+                      void* res_out, int64_t ros, void* stream) {
+    m3_status st = norm_dims_ok(d);
+    if (st != M3_OK) return st;
+    if (!(eps >= 0.f) || std::isinf(eps)) return M3_ERR_SHAPE;
+    if (!res && d->res_dtype != d->io_dtype) return M3_ERR_DTYPE;
+    if (d->rows == 0) return M3_OK;
+    const size_t e = esize(d->io_dtype), er = esize(d->res_dtype);
+    const size_t ey = d->out == M3_OUT_E4M3 ? 1 : e;
+    if ((st = check_mat(x, xs, d, e, true)) != M3_OK || (st = check_mat(res, rs, d, er, false)) != M3_OK ||
+        (st = check_mat(y, ys, d, ey, true)) != M3_OK ||
+        (st = check_mat(res_out, ros, d, er, false)) != M3_OK)
+        return st;
+    if (d->out == M3_OUT_E4M3 && !scales) return M3_ERR_NULL;
+    if ((weight && !at_least(weight, 4)) || (scales && !at_least(scales, 4))) return M3_ERR_ALIGN;
+    NormArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.x = x; a.xs = xs; a.res = res; a.rs = rs; a.weight = weight; a.eps = eps;
+    a.y = y; a.ys = ys; a.scales = scales; a.res_out = res_out; a.ros = ros;
+    a.rows = d->rows; a.d = d->width;
+    a.wide = d->width % 8 == 0 && wide_mat(x, xs, d, e) && wide_mat(res, rs, d, er) &&
+             wide_mat(y, ys, d, ey) && wide_mat(res_out, ros, d, er) && wide_mat(weight, 0, d, 4);
+    return status_of(launch_norm_fwd(a, d->io_dtype, d->res_dtype, d->out,
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+m3_status m3_norm_bwd_workspace_bytes(const m3_norm_dims* d, size_t* bytes) {
+    m3_status st = norm_dims_ok(d);
+    if (st != M3_OK) return st;
+    if (!bytes) return M3_ERR_NULL;
+    const size_t n = sizeof(float) * norm_bwd_shares(d->rows, d->width) * d->width;
+    *bytes = n < 256 ? 256 : (n + 255) / 256 * 256;
+    return M3_OK;
+}
+
+m3_status m3_norm_bwd(const m3_norm_dims* d, const void* r, int64_t rs, const float* weight,
+                      float eps, const void* dy, int64_t dys, const void* dres, int64_t drs,
+                      void* dx, int64_t dxs, void* dresidual, int64_t dros, float* dweight,
+                      void* ws, size_t ws_bytes, void* stream) {
+    m3_status st = norm_dims_ok(d);
+    if (st != M3_OK) return st;
+    if (!(eps >= 0.f) || std::isinf(eps)) return M3_ERR_SHAPE;
+    if (weight && !dweight) return M3_ERR_NULL;
+    if ((weight && !at_least(weight, 4)) || (dweight && !at_least(dweight, 4))) return M3_ERR_ALIGN;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (d->rows == 0) {
+        if (weight && cudaMemsetAsync(dweight, 0, sizeof(float) * d->width, s) != cudaSuccess)
+            return M3_ERR_CUDA;
+        return M3_OK;
+    }
+    const size_t e = esize(d->io_dtype), er = esize(d->res_dtype);
+    if ((st = check_mat(r, rs, d, er, true)) != M3_OK || (st = check_mat(dy, dys, d, e, true)) != M3_OK ||
+        (st = check_mat(dres, drs, d, er, false)) != M3_OK ||
+        (st = check_mat(dx, dxs, d, e, true)) != M3_OK ||
+        (st = check_mat(dresidual, dros, d, er, false)) != M3_OK)
+        return st;
+    size_t need;
+    m3_norm_bwd_workspace_bytes(d, &need);
+    if (weight && (!ws || !at_least(ws, 256) || ws_bytes < need)) return M3_ERR_WORKSPACE;
+    NormArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.x = r; a.xs = rs; a.weight = weight; a.eps = eps; a.dy = dy; a.dys = dys;
+    a.dres = dres; a.drs = drs; a.dx = dx; a.dxs = dxs; a.dresidual = dresidual; a.dros = dros;
+    a.dweight = weight ? dweight : nullptr;
+    a.part = weight ? static_cast<float*>(ws) : nullptr;
+    a.rows = d->rows; a.d = d->width;
+    a.blocks = norm_bwd_blocks(d->rows, d->width);
+    a.wide = d->width % 8 == 0 && wide_mat(r, rs, d, er) && wide_mat(dy, dys, d, e) &&
+             wide_mat(dres, drs, d, er) && wide_mat(dx, dxs, d, e) &&
+             wide_mat(dresidual, dros, d, er) && wide_mat(weight, 0, d, 4);
+    return status_of(launch_norm_bwd(a, d->io_dtype, d->res_dtype, s));
+}
+
+}  // extern "C"

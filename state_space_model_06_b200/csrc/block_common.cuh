@@ -1,0 +1,113 @@
+// block_common.cuh -- shared pieces of the block operators (conv.cu, sel_*.cu, norm.cu): strided
+// row views, vectors of io values, the activations and the lane reductions.
+#pragma once
+
+#include "m3_internal.h"
+
+namespace m3 {
+
+// Device-side form of m3_rows: element (b, t, i) at p[b * bs + t * ts + i].
+template <typename T>
+struct Rows {
+    T* p;
+    long long bs, ts;
+    __device__ __forceinline__ T* at(long long b, long long t) const { return p + b * bs + t * ts; }
+};
+
+// Tokens of sequence b: its entry of seqlens clamped to [0, T], or T.
+__device__ __forceinline__ int tokens_of(const int32_t* seqlens, int b, int T) {
+    return seqlens ? min(max(seqlens[b], 0), T) : T;
+}
+
+// Logistic function.  bf16 results round at 2^-9 (relative), so they take the hardware exp2
+// and reciprocal (a few 2^-22); fp32 results take expf and a rounded division.
+template <typename IO>
+__device__ __forceinline__ float sigmoid_f(float v) {
+    if constexpr (sizeof(IO) == 2) return __fdividef(1.f, 1.f + __expf(-v));
+    return 1.f / (1.f + expf(-v));
+}
+
+// Softplus without overflow: max(v, 0) + log1p(e^-|v|).  The step multiplies every exponent of
+// the recurrence, so it is computed to fp32 rounding for every io type.
+__device__ __forceinline__ float softplus_f(float v) {
+    return fmaxf(v, 0.f) + log1pf(__expf(-fabsf(v)));
+}
+
+__device__ __forceinline__ float ex2(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// V consecutive io values as floats.  WIDE: one aligned vector access of V * sizeof(IO) bytes
+// (8 or 16, or 32 as two); otherwise element by element, the first n of them (the rest read 0
+// and are not written).
+template <typename IO, int V>
+struct Vec {
+    static constexpr int BYTES = V * (int)sizeof(IO);
+    struct alignas(BYTES < 16 ? BYTES : 16) Raw {
+        IO v[V];
+    };
+    template <bool WIDE>
+    static __device__ __forceinline__ void load(float (&f)[V], const IO* p, int n) {
+        if constexpr (WIDE) {
+            if (n > 0) {
+                const Raw r = *reinterpret_cast<const Raw*>(p);
+#pragma unroll
+                for (int i = 0; i < V; i++) f[i] = to_f(r.v[i]);
+                return;
+            }
+#pragma unroll
+            for (int i = 0; i < V; i++) f[i] = 0.f;
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; i++) f[i] = i < n ? to_f(p[i]) : 0.f;
+        }
+    }
+    template <bool WIDE>
+    static __device__ __forceinline__ void store(const float (&f)[V], IO* p, int n) {
+        if constexpr (WIDE) {
+            if (n > 0) {
+                Raw r;
+#pragma unroll
+                for (int i = 0; i < V; i++) r.v[i] = from_f<IO>(f[i]);
+                *reinterpret_cast<Raw*>(p) = r;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; i++)
+                if (i < n) p[i] = from_f<IO>(f[i]);
+        }
+    }
+};
+
+// Sums v[0..M) over the L lanes that differ in the bits LO, 2 LO, .. L LO / 2 of the lane
+// number.  Each halving step keeps half of the values and sends the other half, so the lanes
+// end with max(M / L, 1) sums each: M (1 - 1/L) shuffles instead of M log2 L.  With L >= M the
+// last steps add whole values.  Returns in v[0..max(M/L,1)) the sums of the values whose number
+// starts at the returned offset; lanes that differ only in the adding steps hold the same ones.
+template <int M, int L, int LO, int K>
+__device__ __forceinline__ int lane_sum(float (&v)[K], int lane) {
+    if constexpr (L == 1) {
+        return 0;
+    } else if constexpr (M > 1) {
+        constexpr int H = M / 2, BIT = LO * L / 2;
+        const bool up = lane & BIT;
+#pragma unroll
+        for (int i = 0; i < H; i++) {
+            const float send = up ? v[i] : v[i + H];
+            const float keep = up ? v[i + H] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, BIT);
+        }
+        return (up ? H : 0) + lane_sum<H, L / 2, LO>(v, lane);
+    } else {
+#pragma unroll
+        for (int o = LO * L / 2; o >= LO; o >>= 1) v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+        return 0;
+    }
+}
+
+}  // namespace m3

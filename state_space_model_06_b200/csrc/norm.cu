@@ -1,0 +1,289 @@
+// norm.cu -- RMS norm with the residual's addition, outputs in the io type or in e4m3 with one
+// scale for each 128 values, and its backward (m3_norm_*).
+//
+// Memory alone bounds it: a row is read once, stays in registers between the two passes over
+// its values, and is written once.  A row is spread over TPR threads (a warp to a block of 1024);
+// thread k of a row holds the vectors k, k + TPR, .. of 8 neighbouring values, so the 128 values
+// of an e4m3 group lie in 16 neighbouring lanes.
+#include <cuda_fp8.h>
+
+#include "block_internal.h"
+#include "block_common.cuh"
+
+namespace m3 {
+
+namespace {
+
+constexpr float kAmaxFloor = 7.888609052210118e-31f;   // 2^-100
+constexpr float kE4m3Max = 448.f;
+
+// max that keeps a NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// Sum over the TPR threads of a row of M values each; every thread gets the sums.  `sm` holds
+// M floats for each warp of the block.
+template <int TPR, int M>
+__device__ __forceinline__ void row_sum(float (&v)[M], float* sm) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+        for (int m = 0; m < M; m++) v[m] += __shfl_xor_sync(0xffffffffu, v[m], o);
+    if constexpr (TPR > 32) {
+        constexpr int W = TPR / 32;
+        const int wid = threadIdx.x >> 5, first = wid / W * W;
+        __syncthreads();            // the sums of the row before have been read
+        if ((threadIdx.x & 31) == 0)
+#pragma unroll
+            for (int m = 0; m < M; m++) sm[wid * M + m] = v[m];
+        __syncthreads();
+#pragma unroll
+        for (int m = 0; m < M; m++) {
+            float s = 0.f;
+#pragma unroll
+            for (int w = 0; w < W; w++) s += sm[(first + w) * M + m];
+            v[m] = s;
+        }
+    }
+}
+
+template <typename IO, typename RES, int OUT, int TPR, int NV, bool WIDE>
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_fwd_kernel(const NormArgs a) {
+    constexpr int RPB = TPR < 128 ? 128 / TPR : 1;
+    __shared__ float sm[32];
+    const int k = threadIdx.x % TPR;
+    long long row = (long long)blockIdx.x * RPB + threadIdx.x / TPR;
+    const bool live = row < a.rows;
+    if (!live) row = a.rows - 1;       // a spare row group joins the barriers and writes nothing
+    const IO* x = static_cast<const IO*>(a.x) + row * a.xs;
+    const RES* res = static_cast<const RES*>(a.res) + row * a.rs;
+    float r[NV][8];
+    float ss[1] = {0.f};
+#pragma unroll
+    for (int v = 0; v < NV; v++) {
+        const int i = (k + v * TPR) * 8, n = min(max(a.d - i, 0), 8);
+        Vec<IO, 8>::template load<WIDE>(r[v], x + i, n);
+        if (a.res) {
+            float q[8];
+            Vec<RES, 8>::template load<WIDE>(q, res + i, n);
+#pragma unroll
+            for (int j = 0; j < 8; j++) r[v][j] = to_f(from_f<RES>(r[v][j] + q[j]));
+        }
+#pragma unroll
+        for (int j = 0; j < 8; j++) ss[0] = fmaf(r[v][j], r[v][j], ss[0]);
+    }
+    row_sum<TPR>(ss, sm);
+    const float rstd = 1.f / sqrtf(ss[0] / (float)a.d + a.eps);
+#pragma unroll
+    for (int v = 0; v < NV; v++) {
+        const int i = (k + v * TPR) * 8, n = live ? min(max(a.d - i, 0), 8) : 0;
+        if (a.res_out)
+            Vec<RES, 8>::template store<WIDE>(r[v], static_cast<RES*>(a.res_out) + row * a.ros + i, n);
+        float y[8], w[8];
+        if (a.weight) Vec<float, 8>::load<WIDE>(w, a.weight + i, min(max(a.d - i, 0), 8));
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            y[j] = r[v][j] * rstd;
+            if (a.weight) y[j] *= w[j];
+        }
+        if constexpr (OUT == M3_OUT_IO) {
+            Vec<IO, 8>::template store<WIDE>(y, static_cast<IO*>(a.y) + row * a.ys + i, n);
+        } else {
+            float amax = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; j++) amax = max_nan(amax, fabsf(y[j]));   // padding is 0
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+            const float scale = max_nan(amax, kAmaxFloor) / kE4m3Max;
+            if (n > 0 && i % 128 == 0) a.scales[row * ((a.d + 127) / 128) + i / 128] = scale;
+            // a rounded division, as the definition has it: one ulp would move values that lie
+            // at the middle of two e4m3 steps
+            union { __nv_fp8x2_storage_t h[4]; uint8_t b[8]; uint2 w; } q;
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                q.h[j] = __nv_cvt_float2_to_fp8x2(make_float2(y[2 * j] / scale, y[2 * j + 1] / scale),
+                                                  __NV_SATFINITE, __NV_E4M3);
+            uint8_t* o = static_cast<uint8_t*>(a.y) + row * a.ys + i;
+            if constexpr (WIDE) {
+                if (n > 0) *reinterpret_cast<uint2*>(o) = q.w;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+                    if (j < n) o[j] = q.b[j];
+            }
+        }
+    }
+}
+
+// Backward: a block walks rows (row group `blockIdx.x`, then every gridDim.x-th) and keeps its
+// columns' share of dweight in registers.
+template <typename IO, typename RES, int TPR, int NV, bool WIDE>
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_bwd_kernel(const NormArgs a) {
+    constexpr int RPB = TPR < 128 ? 128 / TPR : 1;
+    __shared__ float sm[64];
+    const int k = threadIdx.x % TPR;
+    float dw[NV][8];
+#pragma unroll
+    for (int v = 0; v < NV; v++)
+#pragma unroll
+        for (int j = 0; j < 8; j++) dw[v][j] = 0.f;
+    const float inv_d = 1.f / (float)a.d;
+    for (long long row0 = (long long)blockIdx.x * RPB; row0 < a.rows; row0 += (long long)gridDim.x * RPB) {
+        long long row = row0 + threadIdx.x / TPR;
+        const bool live = row < a.rows;
+        if (!live) row = a.rows - 1;
+        float r[NV][8], g[NV][8];
+        float s[2] = {0.f, 0.f};      // sum r^2, sum dy w r
+#pragma unroll
+        for (int v = 0; v < NV; v++) {
+            const int i = (k + v * TPR) * 8, n = min(max(a.d - i, 0), 8);
+            Vec<RES, 8>::template load<WIDE>(r[v], static_cast<const RES*>(a.x) + row * a.xs + i, n);
+            Vec<IO, 8>::template load<WIDE>(g[v], static_cast<const IO*>(a.dy) + row * a.dys + i, n);
+            float w[8];
+            if (a.weight) Vec<float, 8>::load<WIDE>(w, a.weight + i, n);
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                s[0] = fmaf(r[v][j], r[v][j], s[0]);
+                s[1] = fmaf(a.weight ? g[v][j] * w[j] : g[v][j], r[v][j], s[1]);
+            }
+        }
+        row_sum<TPR>(s, sm);
+        const float rstd = 1.f / sqrtf(s[0] * inv_d + a.eps);
+        const float back = s[1] * inv_d * rstd * rstd;      // mean(dy w u) rstd
+#pragma unroll
+        for (int v = 0; v < NV; v++) {
+            const int i = (k + v * TPR) * 8, n = live ? min(max(a.d - i, 0), 8) : 0;
+            float w[8], o[8], q[8];
+            if (a.weight) Vec<float, 8>::load<WIDE>(w, a.weight + i, min(max(a.d - i, 0), 8));
+            if (a.dres) Vec<RES, 8>::template load<WIDE>(q, static_cast<const RES*>(a.dres) + row * a.drs + i, n);
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const float gw = a.weight ? g[v][j] * w[j] : g[v][j];
+                o[j] = rstd * (gw - r[v][j] * back);
+                if (a.dres) o[j] += q[j];
+                if (live) dw[v][j] = fmaf(g[v][j], r[v][j] * rstd, dw[v][j]);
+            }
+            Vec<IO, 8>::template store<WIDE>(o, static_cast<IO*>(a.dx) + row * a.dxs + i, n);
+            if (a.dresidual)
+                Vec<RES, 8>::template store<WIDE>(o, static_cast<RES*>(a.dresidual) + row * a.dros + i, n);
+        }
+    }
+    if (a.part) {
+        // row groups of one block add up in a fixed order through the workspace rows
+        const int grp = threadIdx.x / TPR;
+        float* o = a.part + ((long long)blockIdx.x * RPB + grp) * a.d;
+#pragma unroll
+        for (int v = 0; v < NV; v++) {
+            const int i = (k + v * TPR) * 8;
+            Vec<float, 8>::store<WIDE>(dw[v], o + i, min(max(a.d - i, 0), 8));
+        }
+    }
+}
+
+__global__ void __launch_bounds__(256) norm_bwd_sum_kernel(const float* part, int shares, int d,
+                                                           float* dweight) {
+    __shared__ float sm[8][33];
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + lane;
+    float s = 0.f;
+    if (c < d)
+        for (int r = wid; r < shares; r += 8) s += part[(long long)r * d + c];
+    sm[wid][lane] = s;
+    __syncthreads();
+    if (wid == 0 && c < d) {
+        float v = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; i++) v += sm[i][lane];
+        dweight[c] = v;
+    }
+}
+
+// Threads of a row: the fewest that hold it with two vectors each (1024 hold four).
+int row_threads(int d) {
+    int t = 32;
+    while (t < 1024 && t * 8 * 2 < d) t *= 2;
+    return t;
+}
+
+template <typename IO, typename RES, int OUT, bool WIDE>
+cudaError_t fwd_t(const NormArgs& a, cudaStream_t s) {
+    auto go = [&](auto kernel, int tpr) {
+        const int rpb = tpr < 128 ? 128 / tpr : 1;
+        kernel<<<(a.rows + rpb - 1) / rpb, tpr < 128 ? 128 : tpr, 0, s>>>(a);
+        return cudaGetLastError();
+    };
+    switch (row_threads(a.d)) {
+        case 32: return go(norm_fwd_kernel<IO, RES, OUT, 32, 2, WIDE>, 32);
+        case 64: return go(norm_fwd_kernel<IO, RES, OUT, 64, 2, WIDE>, 64);
+        case 128: return go(norm_fwd_kernel<IO, RES, OUT, 128, 2, WIDE>, 128);
+        case 256: return go(norm_fwd_kernel<IO, RES, OUT, 256, 2, WIDE>, 256);
+        case 512: return go(norm_fwd_kernel<IO, RES, OUT, 512, 2, WIDE>, 512);
+    }
+    if (a.d <= 1024 * 16) return go(norm_fwd_kernel<IO, RES, OUT, 1024, 2, WIDE>, 1024);
+    return go(norm_fwd_kernel<IO, RES, OUT, 1024, 4, WIDE>, 1024);
+}
+
+template <typename IO, typename RES, bool WIDE>
+cudaError_t bwd_t(const NormArgs& a, cudaStream_t s) {
+    auto go = [&](auto kernel, int tpr) {
+        kernel<<<a.blocks, tpr < 128 ? 128 : tpr, 0, s>>>(a);
+        if (a.part) {
+            const int rpb = tpr < 128 ? 128 / tpr : 1;
+            norm_bwd_sum_kernel<<<(a.d + 31) / 32, 256, 0, s>>>(a.part, a.blocks * rpb, a.d, a.dweight);
+        }
+        return cudaGetLastError();
+    };
+    switch (row_threads(a.d)) {
+        case 32: return go(norm_bwd_kernel<IO, RES, 32, 2, WIDE>, 32);
+        case 64: return go(norm_bwd_kernel<IO, RES, 64, 2, WIDE>, 64);
+        case 128: return go(norm_bwd_kernel<IO, RES, 128, 2, WIDE>, 128);
+        case 256: return go(norm_bwd_kernel<IO, RES, 256, 2, WIDE>, 256);
+        case 512: return go(norm_bwd_kernel<IO, RES, 512, 2, WIDE>, 512);
+    }
+    if (a.d <= 1024 * 16) return go(norm_bwd_kernel<IO, RES, 1024, 2, WIDE>, 1024);
+    return go(norm_bwd_kernel<IO, RES, 1024, 4, WIDE>, 1024);
+}
+
+template <typename F>
+cudaError_t by_type(int io, int res, bool wide, F f) {
+    using bf = __nv_bfloat16;
+    auto w = [&](auto i, auto r) {
+        return wide ? f(i, r, std::true_type{}) : f(i, r, std::false_type{});
+    };
+    if (io == M3_BF16) return res == M3_BF16 ? w(bf{}, bf{}) : w(bf{}, float{});
+    return res == M3_BF16 ? w(float{}, bf{}) : w(float{}, float{});
+}
+
+}  // namespace
+
+int norm_bwd_blocks(int rows, int d) {
+    const int tpr = row_threads(d), rpb = tpr < 128 ? 128 / tpr : 1, threads = tpr < 128 ? 128 : tpr;
+    const long long groups = ((long long)rows + rpb - 1) / rpb;
+    const int most = 148 * (1024 / threads);
+    return (int)(groups < most ? (groups < 1 ? 1 : groups) : most);
+}
+
+size_t norm_bwd_shares(int rows, int d) {
+    const int tpr = row_threads(d), rpb = tpr < 128 ? 128 / tpr : 1;
+    return (size_t)norm_bwd_blocks(rows, d) * rpb;
+}
+
+cudaError_t launch_norm_fwd(const NormArgs& a, int io, int res, int out, cudaStream_t s) {
+    return by_type(io, res, a.wide, [&](auto i, auto r, auto w) {
+        using I = decltype(i);
+        using R = decltype(r);
+        constexpr bool W = decltype(w)::value;
+        return out == M3_OUT_E4M3 ? fwd_t<I, R, M3_OUT_E4M3, W>(a, s) : fwd_t<I, R, M3_OUT_IO, W>(a, s);
+    });
+}
+
+cudaError_t launch_norm_bwd(const NormArgs& a, int io, int res, cudaStream_t s) {
+    return by_type(io, res, a.wide, [&](auto i, auto r, auto w) {
+        return bwd_t<decltype(i), decltype(r), decltype(w)::value>(a, s);
+    });
+}
+
+}  // namespace m3

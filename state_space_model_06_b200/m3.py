@@ -24,12 +24,19 @@ M3_FLAG_THETA_IS_ANGLE = 1
 M3_FLAG_FORCE_SIMT = 2
 M3_FLAG_TEST_STALL = 4
 M3_FLAG_DEBUG_CHECKS = 8
+M3_FLAG_SILU = 16
+M3_FLAG_DT_SOFTPLUS = 32
+M3_OUT_IO, M3_OUT_E4M3 = 0, 1
 
 EXPORTED = ("m3_state_bytes", "m3_state_init", "m3_scan_workspace_bytes", "m3_scan_fwd",
             "m3_decode_step", "m3_query_status", "m3_scan_fwd_noalloc", "m3_scan_fwd_gated",
             "m3_decode_step_gated", "m3_scan_workspace_bytes_ex", "m3_scan_fwd_ex",
             "m3_decode_step_ex", "m3_scan_bwd_workspace_bytes", "m3_scan_bwd",
-            "m3_scan_bwd_workspace_bytes_ex", "m3_scan_bwd_ex", "m3_status_string")
+            "m3_scan_bwd_workspace_bytes_ex", "m3_scan_bwd_ex",
+            "m3_conv_fwd", "m3_conv_step", "m3_conv_bwd_workspace_bytes", "m3_conv_bwd",
+            "m3_sel_workspace_bytes", "m3_sel_fwd", "m3_sel_step", "m3_sel_bwd_workspace_bytes",
+            "m3_sel_bwd", "m3_norm_fwd", "m3_norm_bwd_workspace_bytes", "m3_norm_bwd",
+            "m3_status_string")
 
 
 class M3Error(RuntimeError):
@@ -63,6 +70,39 @@ class m3_extras(ctypes.Structure):
     _fields_ = [("z", ctypes.c_void_p), ("B_bias", ctypes.c_void_p), ("C_bias", ctypes.c_void_p),
                 ("bc_norm_eps", ctypes.c_float), ("x_expand", ctypes.c_void_p),
                 ("z_expand", ctypes.c_void_p)]
+
+
+class m3_rows(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("batch_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64)]
+
+
+class m3_conv_dims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "channels", "width", "io_dtype")]
+
+
+class m3_conv_grads(ctypes.Structure):
+    _fields_ = [("dx", m3_rows), ("dweight", ctypes.c_void_p), ("dbias", ctypes.c_void_p),
+                ("dstate", ctypes.c_void_p)]
+
+
+class m3_sel_dims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "channels", "ngroups", "dstate",
+                                              "io_dtype")]
+
+
+class m3_sel_inputs(ctypes.Structure):
+    _fields_ = [(n, m3_rows) for n in ("x", "dt", "B", "C", "z")] + \
+        [(n, ctypes.c_void_p) for n in ("A", "D", "dt_bias", "seqlens")]
+
+
+class m3_sel_grads(ctypes.Structure):
+    _fields_ = [(n, m3_rows) for n in ("dx", "ddt", "dB", "dC", "dz")] + \
+        [(n, ctypes.c_void_p) for n in ("dA", "dD", "ddt_bias", "dh")]
+
+
+class m3_norm_dims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rows", "width", "io_dtype", "res_dtype", "out")]
 
 
 _lib = None
@@ -103,6 +143,25 @@ def load_library(path: str = LIB_PATH):
         lib.m3_scan_bwd_ex.argtypes = [dp, i32, vp, vp, vp, vp, vp, vp, vp, vp, sp, ep, vp, vp,
                                        ctypes.POINTER(m3_grads), ctypes.POINTER(m3_extra_grads),
                                        vp, sz, u32, vp]
+        i64, rp = ctypes.c_int64, ctypes.POINTER(m3_rows)
+        cdp, sdp = ctypes.POINTER(m3_conv_dims), ctypes.POINTER(m3_sel_dims)
+        ndp, sip = ctypes.POINTER(m3_norm_dims), ctypes.POINTER(m3_sel_inputs)
+        lib.m3_conv_fwd.argtypes = [cdp, i32, rp, vp, vp, vp, vp, rp, u32, vp]
+        lib.m3_conv_step.argtypes = [cdp, rp, vp, vp, vp, rp, u32, vp]
+        lib.m3_conv_bwd_workspace_bytes.argtypes = [cdp, i32, szp]
+        lib.m3_conv_bwd.argtypes = [cdp, i32, rp, vp, vp, vp, vp, rp,
+                                    ctypes.POINTER(m3_conv_grads), vp, sz, u32, vp]
+        lib.m3_sel_workspace_bytes.argtypes = [sdp, i32, szp]
+        lib.m3_sel_fwd.argtypes = [sdp, i32, sip, vp, rp, vp, sz, u32, vp]
+        lib.m3_sel_step.argtypes = [sdp, sip, vp, rp, u32, vp]
+        lib.m3_sel_bwd_workspace_bytes.argtypes = [sdp, i32, szp]
+        lib.m3_sel_bwd.argtypes = [sdp, i32, sip, vp, rp, vp, ctypes.POINTER(m3_sel_grads), vp, sz,
+                                   u32, vp]
+        lib.m3_norm_fwd.argtypes = [ndp, vp, i64, vp, i64, vp, ctypes.c_float, vp, i64, vp, vp, i64,
+                                    vp]
+        lib.m3_norm_bwd_workspace_bytes.argtypes = [ndp, szp]
+        lib.m3_norm_bwd.argtypes = [ndp, vp, i64, vp, ctypes.c_float, vp, i64, vp, i64, vp, i64, vp,
+                                    i64, vp, vp, sz, vp]
         lib.m3_query_status.argtypes = [vp, vp]
         lib.m3_status_string.argtypes = [ctypes.c_int]
         lib.m3_status_string.restype = ctypes.c_char_p
@@ -414,3 +473,340 @@ def m3_scan_bwd_ex(dims: Dims, seqlen: int, x, B, C, dt, A, lam, theta, D, state
         _ptr(lam), _ptr(theta), _ptr(D), ctypes.byref(st), _ex_ref(ex), _ptr(dy), _ptr(dhT),
         ctypes.byref(g), ctypes.byref(xg), _ptr(workspace), ws_bytes, int(flags),
         _stream(stream)), "m3_scan_bwd_ex")
+
+
+# ---------------------------------------------------------------------------------------------
+# Block operators: short causal convolution, selective scan, residual RMS norm.  Activations may
+# be views (a half of a projection's output): their strides go to the library.  The tensors of a
+# call must agree with its dims in shape and type; a mismatch raises M3Error before anything is
+# launched (the library sees addresses only).  A call runs on its tensors' device, on that
+# device's current stream unless ``stream`` is given.
+
+_F32 = torch.float32
+_TYPE_OF = {M3_F32: torch.float32, M3_BF16: torch.bfloat16}
+
+
+@dataclass
+class ConvDims:
+    batch: int
+    channels: int
+    width: int
+    io_dtype: int = M3_BF16
+
+    def c(self) -> m3_conv_dims:
+        return m3_conv_dims(self.batch, self.channels, self.width, self.io_dtype)
+
+
+@dataclass
+class SelDims:
+    batch: int
+    channels: int
+    ngroups: int
+    dstate: int
+    io_dtype: int = M3_BF16
+
+    def c(self) -> m3_sel_dims:
+        return m3_sel_dims(self.batch, self.channels, self.ngroups, self.dstate, self.io_dtype)
+
+
+@dataclass
+class NormDims:
+    rows: int
+    width: int
+    io_dtype: int = M3_BF16
+    res_dtype: int = M3_BF16
+    out: int = M3_OUT_IO
+
+    def c(self) -> m3_norm_dims:
+        return m3_norm_dims(self.rows, self.width, self.io_dtype, self.res_dtype, self.out)
+
+
+class _Call:
+    """The tensors of one call: checks them against the call's dims, holds their device, and
+    runs the library function there."""
+
+    __slots__ = ("name", "device", "lib")
+
+    def __init__(self, name):
+        self.name, self.device, self.lib = name, None, load_library()
+
+    def _same_device(self, t):
+        if self.device is None:
+            if not t.is_cuda:
+                raise M3Error(M3_ERR_UNSUPPORTED, f"{self.name}: tensors must be on a CUDA device")
+            self.device = t.device
+        elif t.device != self.device:
+            raise M3Error(M3_ERR_UNSUPPORTED, f"{self.name}: tensors on several devices")
+
+    def rows(self, t, lead, width, dtype):
+        """An activation [*lead, *width] (its last axes packed) as m3_rows; lead is (batch,) or
+        (batch, T)."""
+        if t is None:
+            return m3_rows(None, 0, 0)
+        self._same_device(t)
+        if t.dtype != dtype:
+            raise M3Error(M3_ERR_DTYPE, self.name)
+        shape, st, k = t.shape, t.stride(), len(lead)
+        if tuple(shape) != lead + width:
+            raise M3Error(M3_ERR_SHAPE, f"{self.name}: shape {tuple(shape)}, not {lead + width}")
+        packed = 1
+        for n, s in zip(reversed(shape[k:]), reversed(st[k:])):
+            if n > 1 and s != packed:
+                raise M3Error(M3_ERR_SHAPE, f"{self.name}: the last axes must be contiguous")
+            packed *= n
+        return m3_rows(t.data_ptr() or None, st[0], st[1] if k == 2 else 0)
+
+    def packed(self, t, shape, dtype):
+        """A packed tensor's address (None stays None)."""
+        if t is None:
+            return None
+        self._same_device(t)
+        if t.dtype != dtype:
+            raise M3Error(M3_ERR_DTYPE, self.name)
+        if tuple(t.shape) != shape or not t.is_contiguous():
+            raise M3Error(M3_ERR_SHAPE, f"{self.name}: a packed {shape} tensor is expected")
+        return t.data_ptr() or None
+
+    def matrix(self, t, shape, dtype):
+        """A [rows, width] tensor's address and row stride."""
+        if t is None:
+            return None, 0
+        self._same_device(t)
+        if t.dtype not in dtype:
+            raise M3Error(M3_ERR_DTYPE, self.name)
+        st = t.stride()
+        if tuple(t.shape) != shape or (shape[1] > 1 and st[1] != 1):
+            raise M3Error(M3_ERR_SHAPE, f"{self.name}: a {shape} tensor of packed rows is expected")
+        return t.data_ptr() or None, st[0]
+
+    def workspace(self, t):
+        if t is None:
+            return None, 0
+        self._same_device(t)
+        if not t.is_contiguous():
+            raise M3Error(M3_ERR_WORKSPACE, self.name)
+        return t.data_ptr() or None, t.numel() * t.element_size()
+
+    def run(self, stream, *args):
+        fn = getattr(self.lib, self.name)
+        index = self.device.index
+        if index == torch.cuda.current_device():
+            _check(fn(*args, _stream(stream)), self.name)
+        else:
+            with torch.cuda.device(index):
+                _check(fn(*args, _stream(stream)), self.name)
+
+
+def _io_type(dims, name):
+    t = _TYPE_OF.get(dims.io_dtype)
+    if t is None:
+        raise M3Error(M3_ERR_DTYPE, name)
+    return t
+
+
+def _conv_args(call, dims, lead, x, weight, bias, state, seqlens):
+    io, C, W = _io_type(dims, call.name), dims.channels, dims.width
+    return (call.rows(x, lead, (C,), io), call.packed(weight, (C, W), _F32),
+            call.packed(bias, (C,), _F32), call.packed(seqlens, (dims.batch,), torch.int32),
+            call.packed(state, (dims.batch, W - 1, C), io))
+
+
+def m3_conv_fwd(dims: ConvDims, seqlen: int, x, weight, bias, state, y, seqlens=None,
+                flags: int = 0, stream=None):
+    """Short causal convolution of x [b, T, C] into y, carrying ``state`` [b, W-1, C] (updated in
+    place).  ``bias`` and ``seqlens`` (int32 [b]) may be None; flags: M3_FLAG_SILU."""
+    call, lead = _Call("m3_conv_fwd"), (dims.batch, seqlen)
+    xr, w, bi, sl, st = _conv_args(call, dims, lead, x, weight, bias, state, seqlens)
+    yr = call.rows(y, lead, (dims.channels,), _io_type(dims, call.name))
+    call.run(stream, ctypes.byref(dims.c()), int(seqlen), ctypes.byref(xr), w, bi, sl, st,
+             ctypes.byref(yr), int(flags))
+
+
+def m3_conv_step(dims: ConvDims, x, weight, bias, state, y, flags: int = 0, stream=None):
+    """One token of every sequence: x, y [b, C]."""
+    call, lead = _Call("m3_conv_step"), (dims.batch,)
+    xr, w, bi, _, st = _conv_args(call, dims, lead, x, weight, bias, state, None)
+    yr = call.rows(y, lead, (dims.channels,), _io_type(dims, call.name))
+    call.run(stream, ctypes.byref(dims.c()), ctypes.byref(xr), w, bi, st, ctypes.byref(yr),
+             int(flags))
+
+
+def m3_conv_bwd_workspace_bytes(dims: ConvDims, seqlen: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().m3_conv_bwd_workspace_bytes(ctypes.byref(dims.c()), int(seqlen),
+                                                      ctypes.byref(n)),
+           "m3_conv_bwd_workspace_bytes")
+    return n.value
+
+
+def alloc_conv_bwd_workspace(dims: ConvDims, seqlen: int, device="cuda") -> torch.Tensor:
+    return torch.empty(m3_conv_bwd_workspace_bytes(dims, seqlen), dtype=torch.uint8, device=device)
+
+
+def alloc_conv_grads(dims: ConvDims, seqlen: int, device="cuda") -> dict:
+    """Gradient tensors of m3_conv_bwd."""
+    b, C, W = dims.batch, dims.channels, dims.width
+    f = dict(dtype=_F32, device=device)
+    return dict(dx=torch.empty(b, seqlen, C, dtype=torch_dtype_of(dims.io_dtype), device=device),
+                dweight=torch.empty(C, W, **f), dbias=torch.empty(C, **f),
+                dstate=torch.empty(b, W - 1, C, **f))
+
+
+def m3_conv_bwd(dims: ConvDims, seqlen: int, x, weight, bias, state0, dy, grads: dict, workspace,
+                seqlens=None, flags: int = 0, stream=None):
+    """Backward of m3_conv_fwd into ``grads`` (see alloc_conv_grads; dbias is needed with a bias,
+    dstate may be absent); ``state0`` is the state that the forward call started from."""
+    call, lead = _Call("m3_conv_bwd"), (dims.batch, seqlen)
+    io, C, W = _io_type(dims, call.name), dims.channels, dims.width
+    xr, w, bi, sl, st = _conv_args(call, dims, lead, x, weight, bias, state0, seqlens)
+    dyr = call.rows(dy, lead, (C,), io)
+    g = m3_conv_grads(call.rows(grads.get("dx"), lead, (C,), io),
+                      call.packed(grads.get("dweight"), (C, W), _F32),
+                      call.packed(grads.get("dbias"), (C,), _F32),
+                      call.packed(grads.get("dstate"), (dims.batch, W - 1, C), _F32))
+    ws, nb = call.workspace(workspace)
+    call.run(stream, ctypes.byref(dims.c()), int(seqlen), ctypes.byref(xr), w, bi, sl, st,
+             ctypes.byref(dyr), ctypes.byref(g), ws, nb, int(flags))
+
+
+def _sel_inputs(call, dims, lead, x, dt, A, B, C, D, z, dt_bias, seqlens):
+    io, ch, gn = _io_type(dims, call.name), (dims.channels,), (dims.ngroups, dims.dstate)
+    return m3_sel_inputs(
+        call.rows(x, lead, ch, io), call.rows(dt, lead, ch, io), call.rows(B, lead, gn, io),
+        call.rows(C, lead, gn, io), call.rows(z, lead, ch, io),
+        call.packed(A, (dims.channels, dims.dstate), _F32), call.packed(D, ch, _F32),
+        call.packed(dt_bias, ch, _F32), call.packed(seqlens, (dims.batch,), torch.int32))
+
+
+def m3_sel_workspace_bytes(dims: SelDims, seqlen: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().m3_sel_workspace_bytes(ctypes.byref(dims.c()), int(seqlen),
+                                                 ctypes.byref(n)), "m3_sel_workspace_bytes")
+    return n.value
+
+
+def alloc_sel_workspace(dims: SelDims, seqlen: int, device="cuda") -> torch.Tensor:
+    return torch.empty(m3_sel_workspace_bytes(dims, seqlen), dtype=torch.uint8, device=device)
+
+
+def m3_sel_fwd(dims: SelDims, seqlen: int, x, dt, A, B, C, D, z, dt_bias, h, y, workspace,
+               seqlens=None, flags: int = 0, stream=None):
+    """Selective scan of x [b, T, D] into y, carrying h [b, D, N] fp32 (updated in place).
+    dt, z like x; B, C [b, T, G, N]; A [D, N] fp32; D, dt_bias [D] fp32.  D, z, dt_bias, seqlens
+    (int32 [b]) and workspace may be None; flags: M3_FLAG_DT_SOFTPLUS."""
+    call, lead = _Call("m3_sel_fwd"), (dims.batch, seqlen)
+    inp = _sel_inputs(call, dims, lead, x, dt, A, B, C, D, z, dt_bias, seqlens)
+    yr = call.rows(y, lead, (dims.channels,), _io_type(dims, call.name))
+    hp = call.packed(h, (dims.batch, dims.channels, dims.dstate), _F32)
+    ws, nb = call.workspace(workspace)
+    call.run(stream, ctypes.byref(dims.c()), int(seqlen), ctypes.byref(inp), hp, ctypes.byref(yr),
+             ws, nb, int(flags))
+
+
+def m3_sel_step(dims: SelDims, x, dt, A, B, C, D, z, dt_bias, h, y, flags: int = 0, stream=None):
+    """One token of every sequence: x, dt, z, y [b, D]; B, C [b, G, N]."""
+    call, lead = _Call("m3_sel_step"), (dims.batch,)
+    inp = _sel_inputs(call, dims, lead, x, dt, A, B, C, D, z, dt_bias, None)
+    yr = call.rows(y, lead, (dims.channels,), _io_type(dims, call.name))
+    hp = call.packed(h, (dims.batch, dims.channels, dims.dstate), _F32)
+    call.run(stream, ctypes.byref(dims.c()), ctypes.byref(inp), hp, ctypes.byref(yr), int(flags))
+
+
+def m3_sel_bwd_workspace_bytes(dims: SelDims, seqlen: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().m3_sel_bwd_workspace_bytes(ctypes.byref(dims.c()), int(seqlen),
+                                                     ctypes.byref(n)),
+           "m3_sel_bwd_workspace_bytes")
+    return n.value
+
+
+def alloc_sel_bwd_workspace(dims: SelDims, seqlen: int, device="cuda") -> torch.Tensor:
+    return torch.empty(m3_sel_bwd_workspace_bytes(dims, seqlen), dtype=torch.uint8, device=device)
+
+
+def alloc_sel_grads(dims: SelDims, seqlen: int, gate: bool = True, device="cuda") -> dict:
+    """Gradient tensors of m3_sel_bwd (dz with the gate alone)."""
+    b, T, D, G, N = dims.batch, seqlen, dims.channels, dims.ngroups, dims.dstate
+    io = dict(dtype=torch_dtype_of(dims.io_dtype), device=device)
+    f = dict(dtype=_F32, device=device)
+    out = dict(dx=torch.empty(b, T, D, **io), ddt=torch.empty(b, T, D, **io),
+               dB=torch.empty(b, T, G, N, **io), dC=torch.empty(b, T, G, N, **io),
+               dA=torch.empty(D, N, **f), dD=torch.empty(D, **f), ddt_bias=torch.empty(D, **f),
+               dh=torch.empty(b, D, N, **f))
+    if gate:
+        out["dz"] = torch.empty(b, T, D, **io)
+    return out
+
+
+def m3_sel_bwd(dims: SelDims, seqlen: int, x, dt, A, B, C, D, z, dt_bias, h0, dy, dhT,
+               grads: dict, workspace, seqlens=None, flags: int = 0, stream=None):
+    """Backward of m3_sel_fwd into ``grads`` (see alloc_sel_grads; dh may be absent); ``h0`` is
+    the state that the forward call started from, ``dhT`` [b, D, N] fp32 may be None."""
+    call, lead = _Call("m3_sel_bwd"), (dims.batch, seqlen)
+    io, ch, gn = _io_type(dims, call.name), (dims.channels,), (dims.ngroups, dims.dstate)
+    hs = (dims.batch, dims.channels, dims.dstate)
+    inp = _sel_inputs(call, dims, lead, x, dt, A, B, C, D, z, dt_bias, seqlens)
+    dyr = call.rows(dy, lead, ch, io)
+    get = grads.get
+    g = m3_sel_grads(
+        call.rows(get("dx"), lead, ch, io), call.rows(get("ddt"), lead, ch, io),
+        call.rows(get("dB"), lead, gn, io), call.rows(get("dC"), lead, gn, io),
+        call.rows(get("dz"), lead, ch, io),
+        call.packed(get("dA"), (dims.channels, dims.dstate), _F32),
+        call.packed(get("dD"), ch, _F32), call.packed(get("ddt_bias"), ch, _F32),
+        call.packed(get("dh"), hs, _F32))
+    ws, nb = call.workspace(workspace)
+    call.run(stream, ctypes.byref(dims.c()), int(seqlen), ctypes.byref(inp),
+             call.packed(h0, hs, _F32), ctypes.byref(dyr), call.packed(dhT, hs, _F32),
+             ctypes.byref(g), ws, nb, int(flags))
+
+
+def _norm_types(dims, name):
+    if dims.io_dtype not in _TYPE_OF or dims.res_dtype not in _TYPE_OF:
+        raise M3Error(M3_ERR_DTYPE, name)
+    return (_TYPE_OF[dims.io_dtype],), (_TYPE_OF[dims.res_dtype],)
+
+
+def alloc_norm_scales(dims: NormDims, device="cuda") -> torch.Tensor:
+    """The scales of an e4m3 output: one for each 128 values of a row."""
+    return torch.empty(dims.rows, (dims.width + 127) // 128, dtype=_F32, device=device)
+
+
+def m3_norm_fwd(dims: NormDims, x, residual, weight, eps: float, y, scales=None,
+                residual_out=None, stream=None):
+    """r = x + residual (kept in ``residual_out``), y = r / rms(r) * weight.  With M3_OUT_E4M3, y
+    is float8_e4m3fn (or uint8) and ``scales`` [rows, ceil(width / 128)] fp32.  residual, weight
+    and residual_out may be None."""
+    call, shape = _Call("m3_norm_fwd"), (dims.rows, dims.width)
+    io, res = _norm_types(dims, call.name)
+    q = (torch.float8_e4m3fn, torch.uint8) if dims.out == M3_OUT_E4M3 else io
+    args = (*call.matrix(x, shape, io), *call.matrix(residual, shape, res),
+            call.packed(weight, (dims.width,), _F32), float(eps), *call.matrix(y, shape, q),
+            call.packed(scales, (dims.rows, (dims.width + 127) // 128), _F32),
+            *call.matrix(residual_out, shape, res))
+    call.run(stream, ctypes.byref(dims.c()), *args)
+
+
+def m3_norm_bwd_workspace_bytes(dims: NormDims) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().m3_norm_bwd_workspace_bytes(ctypes.byref(dims.c()), ctypes.byref(n)),
+           "m3_norm_bwd_workspace_bytes")
+    return n.value
+
+
+def alloc_norm_bwd_workspace(dims: NormDims, device="cuda") -> torch.Tensor:
+    return torch.empty(m3_norm_bwd_workspace_bytes(dims), dtype=torch.uint8, device=device)
+
+
+def m3_norm_bwd(dims: NormDims, r, weight, eps: float, dy, dres, dx, dresidual, dweight, workspace,
+                stream=None):
+    """Backward of m3_norm_fwd: ``r`` is its residual_out (x without a residual), ``dres`` the
+    gradient of residual_out or None.  dr goes to ``dx`` in the io type and to ``dresidual``
+    (None: not wanted) in the residual's."""
+    call, shape = _Call("m3_norm_bwd"), (dims.rows, dims.width)
+    io, res = _norm_types(dims, call.name)
+    args = (*call.matrix(r, shape, res), call.packed(weight, (dims.width,), _F32), float(eps),
+            *call.matrix(dy, shape, io), *call.matrix(dres, shape, res),
+            *call.matrix(dx, shape, io), *call.matrix(dresidual, shape, res),
+            call.packed(dweight, (dims.width,), _F32), *call.workspace(workspace))
+    call.run(stream, ctypes.byref(dims.c()), *args)
