@@ -75,12 +75,12 @@ m3_status conv_dims_ok(const m3_conv_dims* d) {
     return M3_OK;
 }
 
-// Tokens of a run: long enough that the W - 1 tokens read again at its start cost little, short
-// enough that small calls still spread over the GPU (about four blocks an SM).
-void conv_runs(const m3_conv_dims* d, int32_t T, int most, int* seg, int* nseg) {
-    const int V = 16 / (int)esize(d->io_dtype);
-    const int64_t blocks = (int64_t)d->batch * ((d->channels + 128 * V - 1) / (128 * V));
-    int s = most;
+// Tokens of a run: long enough that the W - 1 tokens read again at its start cost little (64: 5 %
+// from L2 at W 4), short enough that small calls still spread over the GPU.  At least 8, so that
+// only the first run reaches back into the state.
+void conv_runs(const m3_conv_dims* d, int32_t T, int* seg, int* nseg) {
+    const int64_t blocks = (int64_t)d->batch * ((d->channels + 511) / 512);
+    int s = 64;
     while (s > 8 && blocks * ((T + s - 1) / s) < 148 * 4) s /= 2;
     *seg = s;
     *nseg = (T + s - 1) / s;
@@ -113,8 +113,10 @@ void conv_args(ConvArgs* a, const m3_conv_dims* d, int32_t T, const m3_rows* x, 
     a->silu = flags & M3_FLAG_SILU;
 }
 
-bool conv_wide(const m3_conv_dims* d, const void* state) {
-    return d->channels % (16 / (int)esize(d->io_dtype)) == 0 && at_least(state, 16);
+// Four neighbouring channels are one access in every tensor.
+bool conv_wide(const m3_conv_dims* d, const float* weight, const void* state) {
+    return d->channels % (16 / (int)esize(d->io_dtype)) == 0 && at_least(state, 16) &&
+           at_least(weight, 16);
 }
 
 }  // namespace
@@ -136,9 +138,9 @@ m3_status m3_conv_fwd(const m3_conv_dims* d, int32_t T, const m3_rows* x, const 
     ConvArgs a;
     conv_args(&a, d, T, x, weight, bias, seqlens, state, flags);
     set_out(a.y, *y);
-    conv_runs(d, T, 64, &a.seg, &a.nseg);
+    conv_runs(d, T, &a.seg, &a.nseg);
     if ((int64_t)a.batch * a.nseg > kMaxBlocks) return M3_ERR_UNSUPPORTED;
-    a.wide = conv_wide(d, state) && wide_rows(*x, g) && wide_rows(*y, g);
+    a.wide = conv_wide(d, weight, state) && wide_rows(*x, g) && wide_rows(*y, g);
     return status_of(launch_conv(a, ConvCall::fwd, d->io_dtype, static_cast<cudaStream_t>(stream)));
 }
 
@@ -155,7 +157,7 @@ m3_status m3_conv_step(const m3_conv_dims* d, const m3_rows* x, const float* wei
     ConvArgs a;
     conv_args(&a, d, 1, x, weight, bias, nullptr, state, flags);
     set_out(a.y, *y);
-    a.wide = conv_wide(d, state) && wide_rows(*x, g) && wide_rows(*y, g);
+    a.wide = conv_wide(d, weight, state) && wide_rows(*x, g) && wide_rows(*y, g);
     return status_of(launch_conv(a, ConvCall::step, d->io_dtype, static_cast<cudaStream_t>(stream)));
 }
 
@@ -165,7 +167,7 @@ m3_status m3_conv_bwd_workspace_bytes(const m3_conv_dims* d, int32_t T, size_t* 
     if (!bytes) return M3_ERR_NULL;
     if (T < 0) return M3_ERR_SHAPE;
     int seg, nseg;
-    conv_runs(d, T, 128, &seg, &nseg);
+    conv_runs(d, T, &seg, &nseg);
     const size_t n = sizeof(float) * (size_t)d->batch * nseg * (d->width + 1) * d->channels;
     *bytes = n < 256 ? 256 : (n + 255) / 256 * 256;
     return M3_OK;
@@ -208,9 +210,9 @@ m3_status m3_conv_bwd(const m3_conv_dims* d, int32_t T, const m3_rows* x, const 
     a.dbias = bias ? gr->dbias : nullptr;
     a.dstate = gr->dstate;
     a.part = static_cast<float*>(ws);
-    conv_runs(d, T, 128, &a.seg, &a.nseg);
+    conv_runs(d, T, &a.seg, &a.nseg);
     if ((int64_t)a.batch * a.nseg > kMaxBlocks) return M3_ERR_UNSUPPORTED;
-    a.wide = conv_wide(d, state0) && wide_rows(*x, g) && wide_rows(*dy, g) && wide_rows(gr->dx, g);
+    a.wide = conv_wide(d, weight, state0) && wide_rows(*x, g) && wide_rows(*dy, g) && wide_rows(gr->dx, g);
     return status_of(launch_conv(a, ConvCall::bwd, d->io_dtype, s));
 }
 
@@ -262,6 +264,15 @@ void sel_args(SelArgs* a, const m3_sel_dims* d, int32_t T, const m3_sel_inputs* 
     a->softplus = flags & M3_FLAG_DT_SOFTPLUS;
 }
 
+// Whether every row of x, dt, z, B and C, and every group's part of it, starts on 16 bytes and
+// is a multiple of 16 bytes long: tiles then come by asynchronous 16-byte copies.
+bool sel_wide(const m3_sel_dims* d, const Geo& g, const m3_sel_inputs* in) {
+    const int per = 16 / (int)g.e;
+    return d->channels / d->ngroups % per == 0 && d->dstate % per == 0 && wide_rows(in->x, g) &&
+           wide_rows(in->dt, g) && (!in->z.ptr || wide_rows(in->z, g)) && wide_rows(in->B, g) &&
+           wide_rows(in->C, g);
+}
+
 // An upper bound of the blocks of any launch over (tile, segment, batch) or over the states.
 bool sel_grid_ok(const SelArgs& a) {
     const double cells = (double)a.batch * a.D * a.nseg;
@@ -299,6 +310,7 @@ m3_status m3_sel_fwd(const m3_sel_dims* d, int32_t T, const m3_sel_inputs* in, f
     SelArgs a;
     sel_args(&a, d, T, in, h, flags);
     set_out(a.y, *y);
+    a.wide = sel_wide(d, g, in) && wide_rows(*y, g);
     a.nseg = sel_fwd_segments(a.batch, T, a.D, a.G, a.N, &a.seg);
     if (a.nseg > 1 && (!ws || ws_bytes < sel_fwd_workspace(a.batch, T, a.D, a.G, a.N))) a.nseg = 1;
     if (a.nseg == 1) a.seg = T;
@@ -324,6 +336,10 @@ m3_status m3_sel_step(const m3_sel_dims* d, const m3_sel_inputs* in, float* h, c
     a.nseg = 1;
     if ((double)a.batch * a.D / 16 > 2147483646.0) return M3_ERR_UNSUPPORTED;
     a.wide = a.N % 4 == 0 && at_least(h, 16) && at_least(in->A, 16);
+    // four neighbouring states of B and C are one access, and the batch fits a grid's second axis
+    const size_t quad = 4 * g.e;
+    a.step_rows = a.batch <= 65535 && at_least(in->B.ptr, quad) && at_least(in->C.ptr, quad) &&
+                  (a.batch == 1 || (in->B.batch_stride % 4 == 0 && in->C.batch_stride % 4 == 0));
     return status_of(launch_sel_step(a, d->io_dtype, static_cast<cudaStream_t>(stream)));
 }
 

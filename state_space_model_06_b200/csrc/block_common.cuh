@@ -27,11 +27,8 @@ __device__ __forceinline__ float sigmoid_f(float v) {
     return 1.f / (1.f + expf(-v));
 }
 
-// Softplus without overflow: max(v, 0) + log1p(e^-|v|).  The step multiplies every exponent of
-// the recurrence, so it is computed to fp32 rounding for every io type.
-__device__ __forceinline__ float softplus_f(float v) {
-    return fmaxf(v, 0.f) + log1pf(__expf(-fabsf(v)));
-}
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float ex2(float v) {
     float r;
@@ -39,9 +36,49 @@ __device__ __forceinline__ float ex2(float v) {
     return r;
 }
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
+// Softplus: max(v, 0) + log(1 + u), u = e^-|v| in (0, 1].  The step multiplies every exponent of
+// the recurrence, so it is computed to fp32 rounding for every io type.  With s = u / (2 + u) in
+// (0, 1/3], log(1 + u) = 2 atanh(s) = 2 s (1 + s^2/3 + s^4/5 + ..): the four coefficients are a
+// minimax fit of the series over s^2 in [0, 1/9] (relative error 5e-9), good for small u, where
+// log(1 + u) from a rounded 1 + u is not.
+__device__ __forceinline__ float softplus_f(float v) {
+    const float u = ex2(-fabsf(v) * kLog2e);
+    const float s = __fdividef(u, 2.f + u), q = s * s;
+    float r = 0.1400599330663681f;
+    r = fmaf(r, q, 0.1400090307f);
+    r = fmaf(r, q, 0.2001076341f);
+    r = fmaf(r, q, 0.3333320916f);
+    const float t = s + s;
+    return fmaxf(v, 0.f) + fmaf(r * q, t, t);
+}
 
+// ------------------------------------------------------------------ packed pairs
+// Two fp32 values in a 64-bit register pair: one FFMA2 does the work of two FFMAs in one issue
+// slot, and these kernels are short of issue slots.
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pack2(float lo, float hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpack2(f2 v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+    f2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 // V consecutive io values as floats.  WIDE: one aligned vector access of V * sizeof(IO) bytes
 // (8 or 16, or 32 as two); otherwise element by element, the first n of them (the rest read 0
 // and are not written).

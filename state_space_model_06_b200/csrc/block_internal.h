@@ -53,7 +53,7 @@ struct SelArgs {
     float* pD;             // [b * nseg][2][D]: dD, ddt_bias
     int batch, T, D, G, N;
     int seg, nseg;         // tokens per segment (a multiple of the tile), segments
-    bool softplus, wide;
+    bool softplus, wide, step_rows;
 };
 // Tokens of one staged tile: segments are multiples of it.
 constexpr int kSelTile = 32;

@@ -10,9 +10,91 @@ namespace m3 {
 
 namespace {
 
+// Four channels a thread, as two pairs: a pair of fp32 values takes one FFMA2 for its two taps.
+constexpr int V = 4;
+
+template <typename IO>
+struct alignas(V * sizeof(IO)) Quad {
+    IO v[V];
+};
+
+// The n values at p (WIDE: all four, in one access); the rest are zero.
+template <typename IO, bool WIDE>
+__device__ __forceinline__ Quad<IO> load_quad(const IO* p, int n) {
+    if constexpr (WIDE) {
+        return *reinterpret_cast<const Quad<IO>*>(p);
+    } else {
+        Quad<IO> q;
+#pragma unroll
+        for (int i = 0; i < V; i++) q.v[i] = i < n ? p[i] : from_f<IO>(0.f);
+        return q;
+    }
+}
+template <typename IO>
+__device__ __forceinline__ void widen(f2 (&f)[2], const Quad<IO>& q) {
+    f[0] = pack2(to_f(q.v[0]), to_f(q.v[1]));
+    f[1] = pack2(to_f(q.v[2]), to_f(q.v[3]));
+}
+template <typename IO, bool WIDE>
+__device__ __forceinline__ void store_quad(const f2 (&f)[2], IO* p, int n) {
+    float v[V];
+    unpack2(f[0], v[0], v[1]);
+    unpack2(f[1], v[2], v[3]);
+    Vec<IO, V>::template store<WIDE>(v, p, n);
+}
+
+// Taps and bias of a thread's channels: w[k] as pairs of channels.  The V x W weights lie behind
+// each other in memory, so they come as whole 16-byte loads.
+template <int W, bool WIDE>
+__device__ __forceinline__ void load_filter(const ConvArgs& a, int c0, int n, f2 (&w)[W][2], f2 (&bias)[2]) {
+    float f[V * W], bs[V];
+    const float* p = a.weight + (long long)c0 * W;
+    if constexpr (WIDE) {
+#pragma unroll
+        for (int i = 0; i < W; i++) {
+            const float4 q = reinterpret_cast<const float4*>(p)[i];
+            f[4 * i] = q.x; f[4 * i + 1] = q.y; f[4 * i + 2] = q.z; f[4 * i + 3] = q.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V * W; i++) f[i] = i < n * W ? p[i] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < V; i++) bs[i] = a.bias && i < n ? a.bias[c0 + i] : 0.f;
+#pragma unroll
+    for (int k = 0; k < W; k++) {
+        w[k][0] = pack2(f[k], f[W + k]);
+        w[k][1] = pack2(f[2 * W + k], f[3 * W + k]);
+    }
+    bias[0] = pack2(bs[0], bs[1]);
+    bias[1] = pack2(bs[2], bs[3]);
+}
+
+template <typename IO>
+__device__ __forceinline__ f2 silu2(f2 v) {
+    float lo, hi;
+    unpack2(v, lo, hi);
+    return pack2(lo * sigmoid_f<IO>(lo), hi * sigmoid_f<IO>(hi));
+}
+
+// The tokens before t0 into win[0 .. W-2].
+template <typename IO, int W, bool WIDE>
+__device__ __forceinline__ void load_window(const ConvArgs& a, const IO* x, long long ts, const IO* st,
+                                            int t0, int len, int n, f2 (&win)[W][2]) {
+#pragma unroll
+    for (int j = 0; j < W - 1; j++) {
+        const int t = t0 - (W - 1) + j;
+        win[j][0] = win[j][1] = 0;
+        if (t < 0)
+            widen(win[j], load_quad<IO, WIDE>(st + (long long)(t + W - 1) * a.C, n));
+        else if (t < len)
+            widen(win[j], load_quad<IO, WIDE>(x + t * ts, n));
+    }
+}
+
 // ------------------------------------------------------------------ forward
 
-template <typename IO, int W, int V, bool WIDE>
+template <typename IO, int W, bool WIDE>
 __global__ void __launch_bounds__(128) conv_fwd_kernel(const ConvArgs a) {
     const int c0 = (blockIdx.y * blockDim.x + threadIdx.x) * V;
     if (c0 >= a.C) return;
@@ -21,110 +103,115 @@ __global__ void __launch_bounds__(128) conv_fwd_kernel(const ConvArgs a) {
     const int t0 = seg * a.seg;
     const int t1 = min(t0 + a.seg, a.T);
     const int len = tokens_of(a.seqlens, b, a.T);
-    const Rows<const IO> X{static_cast<const IO*>(a.x.p), a.x.bs, a.x.ts};
-    const Rows<IO> Y{static_cast<IO*>(a.y.p), a.y.bs, a.y.ts};
+    const long long xts = a.x.ts, yts = a.y.ts;
+    const IO* x = static_cast<const IO*>(a.x.p) + b * a.x.bs + c0;
+    IO* y = static_cast<IO*>(a.y.p) + b * a.y.bs + c0;
     IO* st = static_cast<IO*>(a.state) + (long long)b * (W - 1) * a.C + c0;
-
-    float w[W][V], bias[V];
-#pragma unroll
-    for (int i = 0; i < V; i++) {
-        bias[i] = (a.bias && i < n) ? a.bias[c0 + i] : 0.f;
-#pragma unroll
-        for (int k = 0; k < W; k++) w[k][i] = i < n ? a.weight[(long long)(c0 + i) * W + k] : 0.f;
-    }
-    // win[j] holds u_{t-W+1+j}; the newest, win[W-1], is the current token
-    float win[W][V];
-#pragma unroll
-    for (int j = 0; j < W - 1; j++) {
-        const int t = t0 - (W - 1) + j;
-        if (t >= 0)
-            Vec<IO, V>::template load<WIDE>(win[j], X.at(b, t) + c0, t < len ? n : 0);
-        else
-            Vec<IO, V>::template load<WIDE>(win[j], st + (long long)(t + W - 1) * a.C, n);
-    }
     const int te = min(t1, len);
-    constexpr int U = 4;      // tokens requested together
-    for (int t = t0; t < te; t += U) {
-        float nx[U][V];
+    constexpr int U = 32 / (int)sizeof(IO) / 2;      // tokens on their way while U others are worked on
+    Quad<IO> next[U];
+    if (t0 < te)
 #pragma unroll
-        for (int u = 0; u < U; u++)
-            Vec<IO, V>::template load<WIDE>(nx[u], X.at(b, min(t + u, te - 1)) + c0, n);
+        for (int u = 0; u < U; u++) next[u] = load_quad<IO, WIDE>(x + min(t0 + u, te - 1) * xts, n);
+
+    f2 w[W][2], bias[2], win[W][2];      // win[j] holds u_{t-W+1+j}
+    load_filter<W, WIDE>(a, c0, n, w, bias);
+    load_window<IO, W, WIDE>(a, x, xts, st, t0, len, n, win);
+    for (int t = t0; t < te; t += U) {
+        Quad<IO> cur[U];
+#pragma unroll
+        for (int u = 0; u < U; u++) cur[u] = next[u];
+        if (t + U < te)
+#pragma unroll
+            for (int u = 0; u < U; u++) next[u] = load_quad<IO, WIDE>(x + min(t + U + u, te - 1) * xts, n);
 #pragma unroll
         for (int u = 0; u < U; u++) {
-            if (t + u < te) {
-                float y[V];
+            f2 s[2];
+            widen(win[W - 1], cur[u]);
 #pragma unroll
-                for (int i = 0; i < V; i++) {
-                    win[W - 1][i] = nx[u][i];
-                    float s = bias[i];
+            for (int i = 0; i < 2; i++) {
+                s[i] = bias[i];
 #pragma unroll
-                    for (int k = 0; k < W; k++) s = fmaf(w[k][i], win[k][i], s);
-                    y[i] = a.silu ? s * sigmoid_f<IO>(s) : s;
+                for (int k = 0; k < W; k++) s[i] = fma2(w[k][i], win[k][i], s[i]);
+                if (a.silu) s[i] = silu2<IO>(s[i]);
 #pragma unroll
-                    for (int k = 0; k < W - 1; k++) win[k][i] = win[k + 1][i];
-                }
-                Vec<IO, V>::template store<WIDE>(y, Y.at(b, t + u) + c0, n);
+                for (int k = 0; k < W - 1; k++) win[k][i] = win[k + 1][i];
             }
+            if (t + u < te) store_quad<IO, WIDE>(s, y + (t + u) * yts, n);
         }
     }
-    const float zero[V] = {};
-    for (int t = max(t0, te); t < t1; t++) Vec<IO, V>::template store<WIDE>(zero, Y.at(b, t) + c0, n);
+    const f2 zero[2] = {0, 0};
+    for (int t = max(t0, te); t < t1; t++) store_quad<IO, WIDE>(zero, y + t * yts, n);
 
-    // The first segment alone reads the state, so it also writes the new one: the last W - 1
+    // The first run alone reads the state, so it also writes the new one: the last W - 1
     // tokens of [state | x], oldest first (place j is u_{len-W+1+j}; each source is at or behind
     // the place that it goes to, and a place is read before a later step writes it).
     if (seg == 0) {
 #pragma unroll
         for (int j = 0; j < W - 1; j++) {
             const int t = len - (W - 1) + j;
-            float v[V];
-            if (t >= 0)
-                Vec<IO, V>::template load<WIDE>(v, X.at(b, t) + c0, n);
-            else
-                Vec<IO, V>::template load<WIDE>(v, st + (long long)(t + W - 1) * a.C, n);
-            Vec<IO, V>::template store<WIDE>(v, st + (long long)j * a.C, n);
+            const Quad<IO> q = load_quad<IO, WIDE>(t >= 0 ? x + t * xts : st + (long long)(t + W - 1) * a.C, n);
+            IO* o = st + (long long)j * a.C;
+            if constexpr (WIDE) {
+                *reinterpret_cast<Quad<IO>*>(o) = q;
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; i++)
+                    if (i < n) o[i] = q.v[i];
+            }
         }
     }
 }
 
 // ------------------------------------------------------------------ one token
 
-template <typename IO, int W, int V, bool WIDE>
-__global__ void __launch_bounds__(128) conv_step_kernel(const ConvArgs a) {
-    const long long per = (a.C + V - 1) / V;
+template <typename IO, int W, bool WIDE>
+__global__ void __launch_bounds__(64) conv_step_kernel(const ConvArgs a) {
+    const int per = (a.C + V - 1) / V;
     const long long id = blockIdx.x * (long long)blockDim.x + threadIdx.x;
-    if (id >= per * a.batch) return;
-    const int b = (int)(id / per), c0 = (int)(id - b * per) * V;
+    if (id >= (long long)per * a.batch) return;
+    const int b = (int)(id / per), c0 = (int)(id - (long long)b * per) * V;
     const int n = min(V, a.C - c0);
     IO* st = static_cast<IO*>(a.state) + (long long)b * (W - 1) * a.C + c0;
-    float win[W][V];
+    Quad<IO> q[W];
 #pragma unroll
-    for (int j = 0; j < W - 1; j++)
-        Vec<IO, V>::template load<WIDE>(win[j], st + (long long)j * a.C, n);
-    Vec<IO, V>::template load<WIDE>(win[W - 1], static_cast<const IO*>(a.x.p) + b * a.x.bs + c0, n);
-    float y[V];
+    for (int j = 0; j < W - 1; j++) q[j] = load_quad<IO, WIDE>(st + (long long)j * a.C, n);
+    q[W - 1] = load_quad<IO, WIDE>(static_cast<const IO*>(a.x.p) + b * a.x.bs + c0, n);
+    f2 w[W][2], s[2];
+    load_filter<W, WIDE>(a, c0, n, w, s);
 #pragma unroll
-    for (int i = 0; i < V; i++) {
-        float s = (a.bias && i < n) ? a.bias[c0 + i] : 0.f;
-#pragma unroll
-        for (int k = 0; k < W; k++)
-            s = fmaf(i < n ? a.weight[(long long)(c0 + i) * W + k] : 0.f, win[k][i], s);
-        y[i] = a.silu ? s * sigmoid_f<IO>(s) : s;
+    for (int k = 0; k < W; k++) {
+        f2 u[2];
+        widen(u, q[k]);
+        s[0] = fma2(w[k][0], u[0], s[0]);
+        s[1] = fma2(w[k][1], u[1], s[1]);
+    }
+    if (a.silu) {
+        s[0] = silu2<IO>(s[0]);
+        s[1] = silu2<IO>(s[1]);
     }
 #pragma unroll
-    for (int j = 0; j < W - 1; j++)
-        Vec<IO, V>::template store<WIDE>(win[j + 1], st + (long long)j * a.C, n);
-    Vec<IO, V>::template store<WIDE>(y, static_cast<IO*>(a.y.p) + b * a.y.bs + c0, n);
+    for (int j = 0; j < W - 1; j++) {
+        IO* o = st + (long long)j * a.C;
+        if constexpr (WIDE) {
+            *reinterpret_cast<Quad<IO>*>(o) = q[j + 1];
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; i++)
+                if (i < n) o[i] = q[j + 1].v[i];
+        }
+    }
+    store_quad<IO, WIDE>(s, static_cast<IO*>(a.y.p) + b * a.y.bs + c0, n);
 }
 
 // ------------------------------------------------------------------ backward
 //
 // g_t = dy_t act'(pre_t);  dx_s = sum_k w[k] g_{s+W-1-k};  dw[k] = sum_t g_t u_{t-W+1+k}.
 // A thread walks the tokens t0 .. t1 + W - 2 of its run, recomputing pre from x.  Its own
-// tokens' g go into dw; dx_s is complete once g_{s+W-1} is known.  The first segment also
+// tokens' g go into dw; dx_s is complete once g_{s+W-1} is known.  The first run also
 // covers s = -(W-1) .. -1, the gradients of the carried tokens.
 
-template <typename IO, int W, int V, bool WIDE>
+template <typename IO, int W, bool WIDE>
 __global__ void __launch_bounds__(128) conv_bwd_kernel(const ConvArgs a) {
     const int c0 = (blockIdx.y * blockDim.x + threadIdx.x) * V;
     if (c0 >= a.C) return;
@@ -133,92 +220,110 @@ __global__ void __launch_bounds__(128) conv_bwd_kernel(const ConvArgs a) {
     const int t0 = seg * a.seg;
     const int t1 = min(t0 + a.seg, a.T);
     const int len = tokens_of(a.seqlens, b, a.T);
-    const Rows<const IO> X{static_cast<const IO*>(a.x.p), a.x.bs, a.x.ts};
-    const Rows<const IO> DY{static_cast<const IO*>(a.dy.p), a.dy.bs, a.dy.ts};
-    const Rows<IO> DX{static_cast<IO*>(a.dx.p), a.dx.bs, a.dx.ts};
+    const long long xts = a.x.ts, gts = a.dy.ts, dts = a.dx.ts;
+    const IO* x = static_cast<const IO*>(a.x.p) + b * a.x.bs + c0;
+    const IO* dy = static_cast<const IO*>(a.dy.p) + b * a.dy.bs + c0;
+    IO* dx = static_cast<IO*>(a.dx.p) + b * a.dx.bs + c0;
     const IO* st = static_cast<const IO*>(a.state) + (long long)b * (W - 1) * a.C + c0;
 
-    float w[W][V], bias[V], dw[W][V], db[V];
+    // the tokens that are looked at: this run's, and W - 1 behind it that only finish its dx
+    const int te = min(t1 + W - 1, len), last = t1 + W - 1;
+    constexpr int U = 4;
+    Quad<IO> nx[U], ng[U];
+    auto request = [&](int t) {
 #pragma unroll
-    for (int i = 0; i < V; i++) {
-        bias[i] = (a.bias && i < n) ? a.bias[c0 + i] : 0.f;
-        db[i] = 0.f;
-#pragma unroll
-        for (int k = 0; k < W; k++) {
-            w[k][i] = i < n ? a.weight[(long long)(c0 + i) * W + k] : 0.f;
-            dw[k][i] = 0.f;
+        for (int u = 0; u < U; u++) {
+            nx[u] = load_quad<IO, WIDE>(x + min(t + u, te - 1) * xts, n);
+            ng[u] = load_quad<IO, WIDE>(dy + min(t + u, te - 1) * gts, n);
         }
-    }
-    float win[W][V];   // u_{t-W+1+j}
-    float acc[W][V];   // acc[j]: dx_{t-W+1+j} so far
+    };
+    if (t0 < te) request(t0);
+    f2 w[W][2], bias[2], win[W][2], dw[W][2], acc[W][2], db[2] = {0, 0};
+    load_filter<W, WIDE>(a, c0, n, w, bias);
+    load_window<IO, W, WIDE>(a, x, xts, st, t0, len, n, win);
 #pragma unroll
-    for (int j = 0; j < W; j++)
+    for (int k = 0; k < W; k++)
 #pragma unroll
-        for (int i = 0; i < V; i++) acc[j][i] = 0.f;
+        for (int i = 0; i < 2; i++) dw[k][i] = acc[k][i] = 0;   // acc[j]: dx_{t-W+1+j} so far
+
+    for (int t = t0; t < last; t += U) {
+        Quad<IO> cx[U], cg[U];
 #pragma unroll
-    for (int j = 0; j < W - 1; j++) {
-        const int t = t0 - (W - 1) + j;
-        if (t >= 0)
-            Vec<IO, V>::template load<WIDE>(win[j], X.at(b, t) + c0, t < len ? n : 0);
-        else
-            Vec<IO, V>::template load<WIDE>(win[j], st + (long long)(t + W - 1) * a.C, n);
-    }
-    // tokens t1 .. t1 + W - 2 only finish this run's dx (they are the next run's own)
-    for (int t = t0; t < t1 + W - 1; t++) {
-        float dy[V];
-        const bool in = t < len;
-        Vec<IO, V>::template load<WIDE>(win[W - 1], X.at(b, min(t, a.T - 1)) + c0, in ? n : 0);
-        Vec<IO, V>::template load<WIDE>(dy, DY.at(b, min(t, a.T - 1)) + c0, in ? n : 0);
-        const bool mine = t < t1;
-#pragma unroll
-        for (int i = 0; i < V; i++) {
-            float g = dy[i];
-            if (a.silu) {
-                float s = bias[i];
-#pragma unroll
-                for (int k = 0; k < W; k++) s = fmaf(w[k][i], win[k][i], s);
-                const float sg = sigmoid_f<IO>(s);
-                g *= sg * (1.f + s * (1.f - sg));
-            }
-            if (!in) g = 0.f;      // past the length: dy is not looked at, 0 * inf stays out
-            const float own = mine ? g : 0.f;
-            db[i] += own;
-#pragma unroll
-            for (int k = 0; k < W; k++) {
-                dw[k][i] = fmaf(own, win[k][i], dw[k][i]);
-                acc[k][i] = fmaf(w[k][i], g, acc[k][i]);
-            }
+        for (int u = 0; u < U; u++) {
+            cx[u] = nx[u];
+            cg[u] = ng[u];
         }
-        // acc[0] is complete: the gradient of token t - W + 1
-        const int s = t - (W - 1);
-        if (s >= t0) {
-            if (s < t1) Vec<IO, V>::template store<WIDE>(acc[0], DX.at(b, s) + c0, n);
-        } else if (seg == 0 && a.dstate) {
-            // s < 0: a carried token (s >= t0 = 0 was taken above)
-            float* o = a.dstate + ((long long)b * (W - 1) + (s + W - 1)) * a.C + c0;
+        if (t + U < te) request(t + U);
 #pragma unroll
-            for (int i = 0; i < V; i++)
-                if (i < n) o[i] = acc[0][i];
-        }
+        for (int u = 0; u < U; u++) {
+            if (t + u < last) {
+                f2 g[2] = {0, 0};
+                win[W - 1][0] = win[W - 1][1] = 0;
+                if (t + u < te) {      // past the length nothing is looked at
+                    widen(win[W - 1], cx[u]);
+                    widen(g, cg[u]);
+                    if (a.silu) {
 #pragma unroll
-        for (int i = 0; i < V; i++) {
+                        for (int i = 0; i < 2; i++) {
+                            f2 s = bias[i];
 #pragma unroll
-            for (int k = 0; k < W - 1; k++) {
-                win[k][i] = win[k + 1][i];
-                acc[k][i] = acc[k + 1][i];
+                            for (int k = 0; k < W; k++) s = fma2(w[k][i], win[k][i], s);
+                            float v[2], d[2];
+                            unpack2(s, v[0], v[1]);
+#pragma unroll
+                            for (int j = 0; j < 2; j++) {
+                                const float sg = sigmoid_f<IO>(v[j]);
+                                d[j] = fmaf(v[j] * sg, 1.f - sg, sg);
+                            }
+                            g[i] = mul2(g[i], pack2(d[0], d[1]));
+                        }
+                    }
+                }
+                const bool mine = t + u < t1;
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    const f2 own = mine ? g[i] : 0;
+                    db[i] = add2(db[i], own);
+#pragma unroll
+                    for (int k = 0; k < W; k++) {
+                        dw[k][i] = fma2(own, win[k][i], dw[k][i]);
+                        acc[k][i] = fma2(w[k][i], g[i], acc[k][i]);
+                    }
+                }
+                // acc[0] is complete: the gradient of token t + u - W + 1
+                const int s = t + u - (W - 1);
+                if (s >= t0) {
+                    store_quad<IO, WIDE>(acc[0], dx + s * dts, n);
+                } else if (s < 0 && a.dstate) {      // a carried token
+                    float v[V];
+                    unpack2(acc[0][0], v[0], v[1]);
+                    unpack2(acc[0][1], v[2], v[3]);
+                    float* o = a.dstate + ((long long)b * (W - 1) + (s + W - 1)) * a.C + c0;
+#pragma unroll
+                    for (int i = 0; i < V; i++)
+                        if (i < n) o[i] = v[i];
+                }
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+#pragma unroll
+                    for (int k = 0; k < W - 1; k++) {
+                        win[k][i] = win[k + 1][i];
+                        acc[k][i] = acc[k + 1][i];
+                    }
+                    acc[W - 1][i] = 0;
+                }
             }
-            acc[W - 1][i] = 0.f;
         }
     }
     // shares of this run: [b * nseg + seg][W + 1][C]
     float* part = a.part + (long long)blockIdx.x * (W + 1) * a.C + c0;
 #pragma unroll
-    for (int i = 0; i < V; i++)
-        if (i < n) {
-#pragma unroll
-            for (int k = 0; k < W; k++) part[(long long)k * a.C + i] = dw[k][i];
-            part[(long long)W * a.C + i] = db[i];
-        }
+    for (int k = 0; k <= W; k++) {
+        float v[V];
+        unpack2(k < W ? dw[k < W ? k : 0][0] : db[0], v[0], v[1]);
+        unpack2(k < W ? dw[k < W ? k : 0][1] : db[1], v[2], v[3]);
+        Vec<float, V>::template store<WIDE>(v, part + (long long)k * a.C, n);
+    }
 }
 
 // Sums the shares over the runs, in a fixed order: a block per 32 channels and tap, its warps
@@ -246,25 +351,22 @@ __global__ void __launch_bounds__(256) conv_bwd_sum_kernel(const float* part, in
 
 template <typename IO, int W, bool WIDE>
 cudaError_t fwd_t(const ConvArgs& a, cudaStream_t s) {
-    constexpr int V = 16 / sizeof(IO);
     const dim3 grid(a.batch * a.nseg, (a.C + 128 * V - 1) / (128 * V));
-    conv_fwd_kernel<IO, W, V, WIDE><<<grid, 128, 0, s>>>(a);
+    conv_fwd_kernel<IO, W, WIDE><<<grid, 128, 0, s>>>(a);
     return cudaGetLastError();
 }
 
 template <typename IO, int W, bool WIDE>
 cudaError_t step_t(const ConvArgs& a, cudaStream_t s) {
-    constexpr int V = WIDE ? 16 / (int)sizeof(IO) : 1;
     const long long n = (long long)a.batch * ((a.C + V - 1) / V);
-    conv_step_kernel<IO, W, V, WIDE><<<(unsigned)((n + 127) / 128), 128, 0, s>>>(a);
+    conv_step_kernel<IO, W, WIDE><<<(unsigned)((n + 63) / 64), 64, 0, s>>>(a);
     return cudaGetLastError();
 }
 
 template <typename IO, int W, bool WIDE>
 cudaError_t bwd_t(const ConvArgs& a, cudaStream_t s) {
-    constexpr int V = 4;
     const dim3 grid(a.batch * a.nseg, (a.C + 128 * V - 1) / (128 * V));
-    conv_bwd_kernel<IO, W, V, WIDE><<<grid, 128, 0, s>>>(a);
+    conv_bwd_kernel<IO, W, WIDE><<<grid, 128, 0, s>>>(a);
     conv_bwd_sum_kernel<<<dim3((a.C + 31) / 32, W + 1), 256, 0, s>>>(
         a.part, a.batch * a.nseg, W, a.C, a.dweight, a.dbias);
     return cudaGetLastError();

@@ -119,10 +119,30 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_fwd_kernel(const N
 }
 
 // Backward: a block walks rows (row group `blockIdx.x`, then every gridDim.x-th) and keeps its
-// columns' share of dweight in registers.
+// columns' share of dweight in registers.  With one vector a thread (rows of up to 8192 values)
+// the next row's r, dy and dres are on their way while a row is summed and written; longer rows
+// are read again for the second pass (from L2), as registers hold dweight alone.
+template <typename IO, typename RES>
+struct BwdVec {
+    typename Vec<RES, 8>::Raw r, q;
+    typename Vec<IO, 8>::Raw g;
+};
+
+template <typename T, bool WIDE>
+__device__ __forceinline__ void load_raw(typename Vec<T, 8>::Raw& v, const T* p, int n) {
+    if constexpr (WIDE) {
+        if (n > 0) v = *reinterpret_cast<const typename Vec<T, 8>::Raw*>(p);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            if (j < n) v.v[j] = p[j];
+    }
+}
+
 template <typename IO, typename RES, int TPR, int NV, bool WIDE>
 __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_bwd_kernel(const NormArgs a) {
     constexpr int RPB = TPR < 128 ? 128 / TPR : 1;
+    constexpr bool AHEAD = NV == 1;
     __shared__ float sm[64];
     const int k = threadIdx.x % TPR;
     float dw[NV][8];
@@ -131,40 +151,69 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_bwd_kernel(const N
 #pragma unroll
         for (int j = 0; j < 8; j++) dw[v][j] = 0.f;
     const float inv_d = 1.f / (float)a.d;
-    for (long long row0 = (long long)blockIdx.x * RPB; row0 < a.rows; row0 += (long long)gridDim.x * RPB) {
-        long long row = row0 + threadIdx.x / TPR;
+    const long long step = (long long)gridDim.x * RPB;
+    auto request = [&](long long row, int v, BwdVec<IO, RES>& to, bool second) {
+        const int i = (k + v * TPR) * 8, n = row < a.rows ? min(max(a.d - i, 0), 8) : 0;
+        load_raw<RES, WIDE>(to.r, static_cast<const RES*>(a.x) + row * a.xs + i, n);
+        load_raw<IO, WIDE>(to.g, static_cast<const IO*>(a.dy) + row * a.dys + i, n);
+        if (second && a.dres)
+            load_raw<RES, WIDE>(to.q, static_cast<const RES*>(a.dres) + row * a.drs + i, n);
+    };
+    auto weights = [&](int v, float (&w)[8]) {
+        const int i = (k + v * TPR) * 8;
+#pragma unroll
+        for (int j = 0; j < 8; j++) w[j] = 1.f;
+        if (a.weight) Vec<float, 8>::load<WIDE>(w, a.weight + i, min(max(a.d - i, 0), 8));
+    };
+    const BwdVec<IO, RES> none = {};
+    long long row = (long long)blockIdx.x * RPB + threadIdx.x / TPR;
+    BwdVec<IO, RES> next = none;
+    float w0[8];
+    weights(0, w0);
+    if (AHEAD) request(row, 0, next, true);
+    // every thread of a block makes the same number of turns: the barriers are the block's
+    for (long long row0 = (long long)blockIdx.x * RPB; row0 < a.rows; row0 += step, row += step) {
         const bool live = row < a.rows;
-        if (!live) row = a.rows - 1;
-        float r[NV][8], g[NV][8];
+        const BwdVec<IO, RES> cur = next;
+        if (AHEAD) {
+            next = none;
+            request(row + step, 0, next, true);
+        }
         float s[2] = {0.f, 0.f};      // sum r^2, sum dy w r
 #pragma unroll
         for (int v = 0; v < NV; v++) {
-            const int i = (k + v * TPR) * 8, n = min(max(a.d - i, 0), 8);
-            Vec<RES, 8>::template load<WIDE>(r[v], static_cast<const RES*>(a.x) + row * a.xs + i, n);
-            Vec<IO, 8>::template load<WIDE>(g[v], static_cast<const IO*>(a.dy) + row * a.dys + i, n);
+            BwdVec<IO, RES> c = AHEAD ? cur : none;
             float w[8];
-            if (a.weight) Vec<float, 8>::load<WIDE>(w, a.weight + i, n);
+            if (!AHEAD) {
+                request(row, v, c, false);
+                weights(v, w);
+            }
 #pragma unroll
             for (int j = 0; j < 8; j++) {
-                s[0] = fmaf(r[v][j], r[v][j], s[0]);
-                s[1] = fmaf(a.weight ? g[v][j] * w[j] : g[v][j], r[v][j], s[1]);
+                const float r = to_f(c.r.v[j]);
+                s[0] = fmaf(r, r, s[0]);
+                s[1] = fmaf(to_f(c.g.v[j]) * (AHEAD ? w0[j] : w[j]), r, s[1]);
             }
         }
         row_sum<TPR>(s, sm);
         const float rstd = 1.f / sqrtf(s[0] * inv_d + a.eps);
         const float back = s[1] * inv_d * rstd * rstd;      // mean(dy w u) rstd
+        if (!live) continue;
 #pragma unroll
         for (int v = 0; v < NV; v++) {
-            const int i = (k + v * TPR) * 8, n = live ? min(max(a.d - i, 0), 8) : 0;
-            float w[8], o[8], q[8];
-            if (a.weight) Vec<float, 8>::load<WIDE>(w, a.weight + i, min(max(a.d - i, 0), 8));
-            if (a.dres) Vec<RES, 8>::template load<WIDE>(q, static_cast<const RES*>(a.dres) + row * a.drs + i, n);
+            const int i = (k + v * TPR) * 8, n = min(max(a.d - i, 0), 8);
+            BwdVec<IO, RES> c = AHEAD ? cur : none;
+            float w[8], o[8];
+            if (!AHEAD) {
+                request(row, v, c, true);
+                weights(v, w);
+            }
 #pragma unroll
             for (int j = 0; j < 8; j++) {
-                const float gw = a.weight ? g[v][j] * w[j] : g[v][j];
-                o[j] = rstd * (gw - r[v][j] * back);
-                if (a.dres) o[j] += q[j];
-                if (live) dw[v][j] = fmaf(g[v][j], r[v][j] * rstd, dw[v][j]);
+                const float r = to_f(c.r.v[j]), g = to_f(c.g.v[j]);
+                o[j] = rstd * (g * (AHEAD ? w0[j] : w[j]) - r * back);
+                if (a.dres) o[j] += to_f(c.q.v[j]);
+                dw[v][j] = fmaf(g, r * rstd, dw[v][j]);
             }
             Vec<IO, 8>::template store<WIDE>(o, static_cast<IO*>(a.dx) + row * a.dxs + i, n);
             if (a.dresidual)
@@ -172,9 +221,8 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_bwd_kernel(const N
         }
     }
     if (a.part) {
-        // row groups of one block add up in a fixed order through the workspace rows
-        const int grp = threadIdx.x / TPR;
-        float* o = a.part + ((long long)blockIdx.x * RPB + grp) * a.d;
+        // the row groups of a block have a row of shares each
+        float* o = a.part + ((long long)blockIdx.x * RPB + threadIdx.x / TPR) * a.d;
 #pragma unroll
         for (int v = 0; v < NV; v++) {
             const int i = (k + v * TPR) * 8;
@@ -226,6 +274,13 @@ cudaError_t fwd_t(const NormArgs& a, cudaStream_t s) {
     return go(norm_fwd_kernel<IO, RES, OUT, 1024, 4, WIDE>, 1024);
 }
 
+// The backward holds four times as much of a row: one vector a thread up to 8192 values.
+int bwd_threads(int d) {
+    int t = 32;
+    while (t < 1024 && t * 8 < d) t *= 2;
+    return t;
+}
+
 template <typename IO, typename RES, bool WIDE>
 cudaError_t bwd_t(const NormArgs& a, cudaStream_t s) {
     auto go = [&](auto kernel, int tpr) {
@@ -236,13 +291,14 @@ cudaError_t bwd_t(const NormArgs& a, cudaStream_t s) {
         }
         return cudaGetLastError();
     };
-    switch (row_threads(a.d)) {
-        case 32: return go(norm_bwd_kernel<IO, RES, 32, 2, WIDE>, 32);
-        case 64: return go(norm_bwd_kernel<IO, RES, 64, 2, WIDE>, 64);
-        case 128: return go(norm_bwd_kernel<IO, RES, 128, 2, WIDE>, 128);
-        case 256: return go(norm_bwd_kernel<IO, RES, 256, 2, WIDE>, 256);
-        case 512: return go(norm_bwd_kernel<IO, RES, 512, 2, WIDE>, 512);
+    switch (bwd_threads(a.d)) {
+        case 32: return go(norm_bwd_kernel<IO, RES, 32, 1, WIDE>, 32);
+        case 64: return go(norm_bwd_kernel<IO, RES, 64, 1, WIDE>, 64);
+        case 128: return go(norm_bwd_kernel<IO, RES, 128, 1, WIDE>, 128);
+        case 256: return go(norm_bwd_kernel<IO, RES, 256, 1, WIDE>, 256);
+        case 512: return go(norm_bwd_kernel<IO, RES, 512, 1, WIDE>, 512);
     }
+    if (a.d <= 1024 * 8) return go(norm_bwd_kernel<IO, RES, 1024, 1, WIDE>, 1024);
     if (a.d <= 1024 * 16) return go(norm_bwd_kernel<IO, RES, 1024, 2, WIDE>, 1024);
     return go(norm_bwd_kernel<IO, RES, 1024, 4, WIDE>, 1024);
 }
@@ -260,14 +316,14 @@ cudaError_t by_type(int io, int res, bool wide, F f) {
 }  // namespace
 
 int norm_bwd_blocks(int rows, int d) {
-    const int tpr = row_threads(d), rpb = tpr < 128 ? 128 / tpr : 1, threads = tpr < 128 ? 128 : tpr;
+    const int tpr = bwd_threads(d), rpb = tpr < 128 ? 128 / tpr : 1, threads = tpr < 128 ? 128 : tpr;
     const long long groups = ((long long)rows + rpb - 1) / rpb;
     const int most = 148 * (1024 / threads);
     return (int)(groups < most ? (groups < 1 ? 1 : groups) : most);
 }
 
 size_t norm_bwd_shares(int rows, int d) {
-    const int tpr = row_threads(d), rpb = tpr < 128 ? 128 / tpr : 1;
+    const int tpr = bwd_threads(d), rpb = tpr < 128 ? 128 / tpr : 1;
     return (size_t)norm_bwd_blocks(rows, d) * rpb;
 }
 

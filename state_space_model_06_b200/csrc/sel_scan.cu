@@ -15,111 +15,221 @@ namespace m3 {
 
 namespace {
 
-// One block: CB channels of one group over one segment.  LOCAL: the segment's own end state from
-// no entry state, and its sum of delta (no y).  Otherwise the outputs, from the entry state in
-// hseg (segmented) or in h.
-template <typename IO, typename SH, bool LOCAL>
+// One block: CB channels of one group over one segment, L tokens at a time.  While a tile is
+// worked on, the next one's x, dt, z, B and C are on their way to the other half of the raw
+// buffers.  Of each tile delta, delta x and the fp32 B and C are laid out first, once for all
+// the lanes that share them.
+// LOCAL: the segment's own end state from no entry state, and its sum of delta (no y).
+// Otherwise the outputs, from the entry state in hseg (segmented) or in h.
+//
+// A lane holds NT states of two neighbouring channels.  What limits the choice: the exponential
+// unit takes 8 cycles for 32 of them (a channel-token of 16 states on 32 lanes: 170 cycles of a
+// sub-partition with softplus and gate), a broadcast 16-byte read of B or C takes 4 cycles of the
+// SM's shared memory however few lanes differ, and a warp alone cannot keep the exponential unit
+// busy.  Two channels a lane halve the reads of B and C; four states a lane leave enough warps.
+template <typename IO, typename SH>
+struct FwdSmem {
+    static constexpr int L = SH::L, CB = SH::CB * 2;
+    // B and C rows keep a multiple of 16 bytes
+    static constexpr int NR = (SH::NP * (int)sizeof(IO) + 15) / 16 * 16 / (int)sizeof(IO);
+    struct Raw {
+        alignas(16) IO x[L][CB], dt[L][CB], z[L][CB], B[L][NR], C[L][NR];
+    };
+    Raw raw[2];
+    alignas(16) float bc[L][2][SH::NP];
+    alignas(16) float4 dd[L][CB / 2];     // of two channels: delta, delta, delta x, delta x
+};
+
+template <typename IO>
+__device__ __forceinline__ float2 pair_of(const IO* p) {
+    if constexpr (sizeof(IO) == 2) {
+        return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p));
+    } else {
+        return *reinterpret_cast<const float2*>(p);
+    }
+}
+
+template <typename IO, typename SH, bool WIDE, bool LOCAL>
 __global__ void __launch_bounds__(SH::THREADS) sel_scan_kernel(const SelArgs a) {
-    constexpr int L = SH::L, NT = SH::NT, S = SH::S, CW = SH::CW, CB = SH::CB, NP = SH::NP;
-    __shared__ alignas(16) float bc[L * 2 * NP];
-    __shared__ float2 dd[L][CB];     // delta, delta * x
+    constexpr int L = SH::L, NT = SH::NT, S = SH::S, CW = SH::CW, CB = SH::CB * 2, NP = SH::NP;
+    constexpr int THREADS = SH::THREADS;
+    using Smem = FwdSmem<IO, SH>;
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
     const SelPlace p = sel_place(a, CB);
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    const int cl = wid * CW + lane % CW;     // channel within the block
+    const int pl = wid * CW + lane % CW;     // pair of channels within the block
     const int s = lane / CW;                 // which NT states
-    const bool live = cl < p.nc;
-    const int c = p.c0 + cl;
+    const int c = p.c0 + 2 * pl;
+    const int mine = min(max(p.nc - 2 * pl, 0), 2);     // channels of the pair that exist
+    const int end = min(p.t1, p.len);
 
-    float h[NT], A2[NT];
+    auto request = [&](int t0, typename Smem::Raw& r) {
+        const long long bn = (long long)p.g * a.N;
+        stage_rows<IO, WIDE, L, CB, THREADS>(&r.x[0][0], a.x, p.b, p.c0, t0, end, p.nc);
+        stage_rows<IO, WIDE, L, CB, THREADS>(&r.dt[0][0], a.dt, p.b, p.c0, t0, end, p.nc);
+        if (!LOCAL && a.z.p)
+            stage_rows<IO, WIDE, L, CB, THREADS>(&r.z[0][0], a.z, p.b, p.c0, t0, end, p.nc);
+        stage_rows<IO, WIDE, L, Smem::NR, THREADS>(&r.B[0][0], a.B, p.b, bn, t0, end, a.N);
+        if (!LOCAL)
+            stage_rows<IO, WIDE, L, Smem::NR, THREADS>(&r.C[0][0], a.C, p.b, bn, t0, end, a.N);
+    };
+    if (p.t0 < end) request(p.t0, sm.raw[0]);
+    cp_async_commit();
+
+    f2 h[2][NT / 2], A2[2][NT / 2];      // pairs of neighbouring states
     const long long row = ((long long)p.b * a.D + c) * a.N;
     const long long rowseg = (((long long)p.b * a.nseg + p.seg) * a.D + c) * a.N;
 #pragma unroll
-    for (int i = 0; i < NT; i++) {
-        const int n = s * NT + i;
-        const bool on = live && n < a.N;
-        A2[i] = on ? a.A[(long long)c * a.N + n] * kLog2e : 0.f;
-        h[i] = 0.f;
-        if (!LOCAL && on) h[i] = a.nseg > 1 ? a.hseg[rowseg + n] : a.h[row + n];
-    }
-    float total = 0.f;
-    const int end = min(p.t1, p.len);
-    const Rows<const IO> X{static_cast<const IO*>(a.x.p), a.x.bs, a.x.ts};
-    const Rows<const IO> DT{static_cast<const IO*>(a.dt.p), a.dt.bs, a.dt.ts};
-    const Rows<const IO> Z{static_cast<const IO*>(a.z.p), a.z.bs, a.z.ts};
+    for (int q = 0; q < 2; q++)
+#pragma unroll
+        for (int i = 0; i < NT / 2; i++) {
+            float hv[2] = {0.f, 0.f}, av[2] = {0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                const int n = s * NT + 2 * i + j;
+                if (q < mine && n < a.N) {
+                    av[j] = a.A[(long long)(c + q) * a.N + n] * kLog2e;
+                    if (!LOCAL)
+                        hv[j] = a.nseg > 1 ? a.hseg[rowseg + q * a.N + n] : a.h[row + q * a.N + n];
+                }
+            }
+            A2[q][i] = pack2(av[0], av[1]);
+            h[q][i] = pack2(hv[0], hv[1]);
+        }
+    float skip[2] = {0.f, 0.f};
+    if (a.Dskip)
+#pragma unroll
+        for (int q = 0; q < 2; q++)
+            if (q < mine) skip[q] = a.Dskip[c + q];
+    // the pair of channels whose deltas this thread lays out
+    static_assert(THREADS % (CB / 2) == 0, "");
+    const int kd = threadIdx.x % (CB / 2);
+    float bias[2] = {0.f, 0.f};
+    if (a.dt_bias)
+#pragma unroll
+        for (int q = 0; q < 2; q++)
+            if (2 * kd + q < p.nc) bias[q] = a.dt_bias[p.c0 + 2 * kd + q];
+    float total[2] = {0.f, 0.f};
     const Rows<IO> Y{static_cast<IO*>(a.y.p), a.y.bs, a.y.ts};
 
-    for (int t0 = p.t0; t0 < end; t0 += L) {
-        __syncthreads();
-        sel_stage_bc<IO, NP, L, SH::THREADS>(a, p, t0, end, bc);
-        for (int i = threadIdx.x; i < L * CB; i += SH::THREADS) {
-            const int k = i % CB, t = t0 + i / CB;
-            float2 v = make_float2(0.f, 0.f);
-            if (t < end && k < p.nc) {
-                v.x = sel_delta(to_f(DT.at(p.b, t)[p.c0 + k]), a.dt_bias ? a.dt_bias[p.c0 + k] : 0.f,
-                                a.softplus);
-                v.y = v.x * to_f(X.at(p.b, t)[p.c0 + k]);
+    int stage = 0;
+    for (int t0 = p.t0; t0 < end; t0 += L, stage ^= 1) {
+        cp_async_wait<0>();
+        __syncthreads();     // this tile has arrived; the one before is done with
+        const typename Smem::Raw& r = sm.raw[stage];
+        if (t0 + L < end) request(t0 + L, sm.raw[stage ^ 1]);
+        cp_async_commit();
+#pragma unroll 4
+        for (int i = threadIdx.x; i < L * NP; i += THREADS) {
+            const int u = i / NP, n = i % NP;
+            sm.bc[u][0][n] = n < a.N ? to_f(r.B[u][n]) : 0.f;
+            if (!LOCAL) sm.bc[u][1][n] = n < a.N ? to_f(r.C[u][n]) : 0.f;
+        }
+#pragma unroll 4
+        for (int u = threadIdx.x / (CB / 2); u < L; u += THREADS / (CB / 2)) {
+            float2 delta = make_float2(0.f, 0.f), dx = delta;
+            if (t0 + u < end) {
+                const float2 dt = pair_of(&r.dt[u][2 * kd]), x = pair_of(&r.x[u][2 * kd]);
+                delta.x = sel_delta(dt.x, bias[0], a.softplus);
+                delta.y = sel_delta(dt.y, bias[1], a.softplus);
+                dx.x = delta.x * x.x;
+                dx.y = delta.y * x.y;
             }
-            dd[i / CB][k] = v;
+            sm.dd[u][kd] = make_float4(delta.x, delta.y, dx.x, dx.y);
         }
         __syncthreads();
         const int count = min(L, end - t0);
         for (int u0 = 0; u0 < count; u0 += S) {
-            float y[S];
+            // G tokens at a time: first what depends on no state (the decays and the inputs),
+            // then the chain through the states, so that the exponentials of several tokens
+            // are in flight together
+            constexpr int G = SH::GT < S ? SH::GT : S;
+            float y[2 * S];
 #pragma unroll
-            for (int u = 0; u < S; u++) {
-                const float2 d = dd[u0 + u][cl];       // zero past the end: h stays
-                const float4* pb = reinterpret_cast<const float4*>(bc + (u0 + u) * 2 * NP + s * NT);
-                const float4* pc = reinterpret_cast<const float4*>(bc + ((u0 + u) * 2 + 1) * NP + s * NT);
-                float acc = 0.f;
+            for (int g0 = 0; g0 < S; g0 += G) {
+                f2 dec[G][2][NT / 2], in[G][2][NT / 2];
 #pragma unroll
-                for (int q = 0; q < NT / 4; q++) {
-                    const float4 B4 = pb[q];
-                    float4 C4;
-                    if (!LOCAL) C4 = pc[q];
-                    const float Bv[4] = {B4.x, B4.y, B4.z, B4.w};
-                    const float Cv[4] = {C4.x, C4.y, C4.z, C4.w};
+                for (int g = 0; g < G; g++) {
+                    const int u = u0 + g0 + g;
+                    const float4 d = sm.dd[u][pl];       // zero past the end: h stays
+                    f2 B[NT / 2];
+                    load_pairs(B, &sm.bc[u][0][s * NT]);
 #pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        const int i = q * 4 + j;
-                        h[i] = fmaf(ex2(d.x * A2[i]), h[i], d.y * Bv[j]);
-                        if (!LOCAL) acc = fmaf(Cv[j], h[i], acc);
+                    for (int i = 0; i < NT / 2; i++) {
+                        dec[g][0][i] = ex2_2(mul2(pack2(d.x, d.x), A2[0][i]));
+                        dec[g][1][i] = ex2_2(mul2(pack2(d.y, d.y), A2[1][i]));
+                        in[g][0][i] = mul2(pack2(d.z, d.z), B[i]);
+                        in[g][1][i] = mul2(pack2(d.w, d.w), B[i]);
+                    }
+                    if (LOCAL) {
+                        total[0] += d.x;
+                        total[1] += d.y;
                     }
                 }
-                y[u] = acc;
-                if (LOCAL) total += d.x;
+#pragma unroll
+                for (int g = 0; g < G; g++) {
+                    f2 C[NT / 2], acc[2];
+                    if (!LOCAL) load_pairs(C, &sm.bc[u0 + g0 + g][1][s * NT]);
+#pragma unroll
+                    for (int i = 0; i < NT / 2; i++)
+#pragma unroll
+                        for (int q = 0; q < 2; q++) {
+                            h[q][i] = fma2(dec[g][q][i], h[q][i], in[g][q][i]);
+                            if (!LOCAL)
+                                acc[q] = i == 0 ? mul2(C[i], h[q][i]) : fma2(C[i], h[q][i], acc[q]);
+                        }
+                    if (!LOCAL) {
+#pragma unroll
+                        for (int q = 0; q < 2; q++) {
+                            float lo, hi;
+                            unpack2(acc[q], lo, hi);
+                            y[2 * (g0 + g) + q] = lo + hi;
+                        }
+                    }
+                }
             }
             if (!LOCAL) {
-                // lanes of one channel: each ends with the sum of one of the S tokens
-                const int u = u0 + lane_sum<S, S, CW>(y, lane);
+                // lanes of one pair of channels: each ends with the sums of one of the S tokens
+                const int u = u0 + lane_sum<2 * S, S, CW>(y, lane) / 2;
                 const int t = t0 + u;
-                if (live && t < end) {
-                    float v = y[0];
-                    if (a.Dskip) v = fmaf(a.Dskip[c], to_f(X.at(p.b, t)[c]), v);
+                if (mine && t < end) {
+                    const float2 x = pair_of(&r.x[u][2 * pl]);
+                    float v[2] = {fmaf(skip[0], x.x, y[0]), fmaf(skip[1], x.y, y[1])};
                     if (a.z.p) {
-                        const float z = to_f(Z.at(p.b, t)[c]);
-                        v *= z * sigmoid_f<IO>(z);
+                        const float2 z = pair_of(&r.z[u][2 * pl]);
+                        v[0] *= z.x * sigmoid_f<IO>(z.x);
+                        v[1] *= z.y * sigmoid_f<IO>(z.y);
                     }
-                    Y.at(p.b, t)[c] = from_f<IO>(v);
+                    Vec<IO, 2>::template store<WIDE>(v, Y.at(p.b, t) + c, mine);
                 }
             }
         }
     }
+    cp_async_wait<0>();
     if (!LOCAL)       // rows past the sequence's length
         for (int t = max(p.t0, p.len); t < p.t1; t++)
-            for (int k = threadIdx.x; k < p.nc; k += SH::THREADS)
+            for (int k = threadIdx.x; k < p.nc; k += THREADS)
                 Y.at(p.b, t)[p.c0 + k] = from_f<IO>(0.f);
-    if (live) {
 #pragma unroll
-        for (int i = 0; i < NT; i++) {
-            const int n = s * NT + i;
-            if (n < a.N) {
-                if (LOCAL)
-                    a.hseg[rowseg + n] = h[i];
-                else if (p.seg == a.nseg - 1)
-                    a.h[row + n] = h[i];
+    for (int q = 0; q < 2; q++) {
+        if (q >= mine) break;
+#pragma unroll
+        for (int i = 0; i < NT / 2; i++) {
+            float hv[2];
+            unpack2(h[q][i], hv[0], hv[1]);
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                const int n = s * NT + 2 * i + j;
+                if (n < a.N) {
+                    if (LOCAL)
+                        a.hseg[rowseg + q * a.N + n] = hv[j];
+                    else if (p.seg == a.nseg - 1)
+                        a.h[row + q * a.N + n] = hv[j];
+                }
             }
         }
-        if (LOCAL && s == 0) a.dsum[((long long)p.b * a.nseg + p.seg) * a.D + c] = total;
+        if (LOCAL && s == 0) a.dsum[((long long)p.b * a.nseg + p.seg) * a.D + c + q] = total[q];
     }
 }
 
@@ -142,6 +252,11 @@ __global__ void __launch_bounds__(256) sel_chain_kernel(const SelArgs a) {
 }
 
 // One token: SL lanes share a channel, each taking 4 states at a time.
+template <typename IO>
+struct alignas(4 * sizeof(IO)) Quad4 {
+    IO v[4];
+};
+
 template <typename IO, int SL, bool WIDE>
 __global__ void __launch_bounds__(128) sel_step_kernel(const SelArgs a) {
     const long long cell = (blockIdx.x * 128ll + threadIdx.x) / SL;
@@ -188,31 +303,145 @@ __global__ void __launch_bounds__(128) sel_step_kernel(const SelArgs a) {
     }
 }
 
-template <typename IO, typename SH>
-cudaError_t fwd_t(const SelArgs& a, cudaStream_t s) {
-    const unsigned grid = (unsigned)((long long)sel_tiles(a.D, a.G, SH::CB) * a.nseg * a.batch);
+// One token for N = 4 SL up to 32 and rows on 16 bytes: SL lanes share a channel, four states
+// each.  A warp takes 32 channels of ROWS sequences: each lane loads and prepares one channel's
+// x, dt and z; then SL turns go over 32 / SL channels each, whose states are one contiguous
+// stretch of memory.  A stays in registers over the sequences; the next sequence's states are on
+// their way while one is worked on.
+template <typename IO, int SL, int ROWS>
+__global__ void __launch_bounds__(128) sel_step_rows_kernel(const SelArgs a) {
+    const int lane = threadIdx.x & 31, k = lane / SL, s = lane % SL;
+    constexpr int CW = 32 / SL;                       // channels of a turn
+    const int per_g = a.D / a.G, tiles_g = (per_g + 31) / 32;
+    const int tile = blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (tile >= tiles_g * a.G) return;
+    const int g = tile / tiles_g, c0 = g * per_g + (tile - g * tiles_g) * 32;
+    const int nc = min(32, (g + 1) * per_g - c0);     // channels of this warp
+    const int b0 = blockIdx.y * ROWS, b1 = min(b0 + ROWS, a.batch);
+    const int own = CW * s + k;                       // the channel this lane prepares and writes
+    const bool mine = own < nc;
+    const int c = c0 + (mine ? own : 0);
+    const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, skip = a.Dskip ? a.Dskip[c] : 0.f;
+    float4 A[SL], next[SL];
+    auto states = [&](int b, int i) {
+        return a.h + ((long long)b * a.D + c0 + i * CW + k) * (4 * SL) + 4 * s;
+    };
+    struct Token { IO x, dt, z; Quad4<IO> B, C; } tok;
+    auto request = [&](int b) {
+#pragma unroll
+        for (int i = 0; i < SL; i++) {
+            next[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i * CW + k < nc) next[i] = *reinterpret_cast<const float4*>(states(b, i));
+        }
+        tok.x = (static_cast<const IO*>(a.x.p) + b * a.x.bs)[c];
+        tok.dt = (static_cast<const IO*>(a.dt.p) + b * a.dt.bs)[c];
+        if (a.z.p) tok.z = (static_cast<const IO*>(a.z.p) + b * a.z.bs)[c];
+        const long long at = (long long)g * a.N + 4 * s;
+        tok.B = *reinterpret_cast<const Quad4<IO>*>(static_cast<const IO*>(a.B.p) + b * a.B.bs + at);
+        tok.C = *reinterpret_cast<const Quad4<IO>*>(static_cast<const IO*>(a.C.p) + b * a.C.bs + at);
+    };
+    request(b0);
+#pragma unroll
+    for (int i = 0; i < SL; i++) {
+        A[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i * CW + k < nc) {
+            A[i] = *reinterpret_cast<const float4*>(a.A + (long long)(c0 + i * CW + k) * a.N + 4 * s);
+            A[i].x *= kLog2e; A[i].y *= kLog2e; A[i].z *= kLog2e; A[i].w *= kLog2e;
+        }
+    }
+    for (int b = b0; b < b1; b++) {
+        const float x = to_f(tok.x), delta = sel_delta(to_f(tok.dt), bias, a.softplus), dx = delta * x;
+        const float z = a.z.p ? to_f(tok.z) : 0.f;
+        float Bv[4], Cv[4];
+        float4 h[SL];
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            Bv[j] = to_f(tok.B.v[j]);
+            Cv[j] = to_f(tok.C.v[j]);
+        }
+#pragma unroll
+        for (int i = 0; i < SL; i++) h[i] = next[i];
+        if (b + 1 < b1) request(b + 1);
+        float y[SL];
+#pragma unroll
+        for (int i = 0; i < SL; i++) {
+            // turn i works on channel i CW + k, which lane k SL + i of this warp prepared
+            const float d = __shfl_sync(0xffffffffu, delta, k * SL + i);
+            const float u = __shfl_sync(0xffffffffu, dx, k * SL + i);
+            h[i].x = fmaf(ex2(d * A[i].x), h[i].x, u * Bv[0]);
+            h[i].y = fmaf(ex2(d * A[i].y), h[i].y, u * Bv[1]);
+            h[i].z = fmaf(ex2(d * A[i].z), h[i].z, u * Bv[2]);
+            h[i].w = fmaf(ex2(d * A[i].w), h[i].w, u * Bv[3]);
+            y[i] = fmaf(Cv[0], h[i].x, fmaf(Cv[1], h[i].y, fmaf(Cv[2], h[i].z, Cv[3] * h[i].w)));
+            if (i * CW + k < nc) *reinterpret_cast<float4*>(states(b, i)) = h[i];
+        }
+        lane_sum<SL, SL, 1>(y, lane);      // lane k SL + i ends with channel i CW + k: its own
+        if (mine) {
+            float v = fmaf(skip, x, y[0]);
+            if (a.z.p) v *= z * sigmoid_f<IO>(z);
+            (static_cast<IO*>(a.y.p) + b * a.y.bs)[c] = from_f<IO>(v);
+        }
+    }
+}
+
+template <typename IO, typename SH, bool WIDE>
+cudaError_t fwd_w(const SelArgs& a, cudaStream_t s) {
+    constexpr int bytes = (int)sizeof(FwdSmem<IO, SH>);
+    static_assert(bytes <= 227 * 1024, "");
+    const unsigned grid = (unsigned)((long long)sel_tiles(a.D, a.G, 2 * SH::CB) * a.nseg * a.batch);
+    cudaError_t e = cudaFuncSetAttribute(sel_scan_kernel<IO, SH, WIDE, false>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
     if (a.nseg > 1) {
-        sel_scan_kernel<IO, SH, true><<<grid, SH::THREADS, 0, s>>>(a);
+        e = cudaFuncSetAttribute(sel_scan_kernel<IO, SH, WIDE, true>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
+        sel_scan_kernel<IO, SH, WIDE, true><<<grid, SH::THREADS, bytes, s>>>(a);
         const long long n = (long long)a.batch * a.D * a.N;
         sel_chain_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(a);
     }
-    sel_scan_kernel<IO, SH, false><<<grid, SH::THREADS, 0, s>>>(a);
+    sel_scan_kernel<IO, SH, WIDE, false><<<grid, SH::THREADS, bytes, s>>>(a);
     return cudaGetLastError();
 }
 
-template <typename IO>
-cudaError_t fwd_by_n(const SelArgs& a, cudaStream_t s) {
-    if (a.N <= 4) return fwd_t<IO, SelShape<4, 1, 4>>(a, s);
-    if (a.N <= 8) return fwd_t<IO, SelShape<8, 1, 4>>(a, s);
-    if (a.N <= 16) return fwd_t<IO, SelShape<8, 2, 4>>(a, s);
-    if (a.N <= 32) return fwd_t<IO, SelShape<8, 4, 4>>(a, s);
-    if (a.N <= 64) return fwd_t<IO, SelShape<8, 8, 4>>(a, s);
-    if (a.N <= 128) return fwd_t<IO, SelShape<8, 16, 4>>(a, s);
-    return fwd_t<IO, SelShape<16, 16, 4, 16>>(a, s);
+template <typename IO, typename SH>
+cudaError_t fwd_t(const SelArgs& a, cudaStream_t s) {
+    return a.wide ? fwd_w<IO, SH, true>(a, s) : fwd_w<IO, SH, false>(a, s);
+}
+
+// The lane shape of a forward call, by the number of states.
+template <typename F>
+auto fwd_shape(int N, F f) {
+    if (N <= 4) return f(SelShape<4, 1, 2, 16>{});
+    if (N <= 8) return f(SelShape<4, 2, 2, 32>{});
+    if (N <= 16) return f(SelShape<2, 8, 4, 32, 2>{});
+    if (N <= 32) return f(SelShape<4, 8, 4, 32>{});
+    if (N <= 64) return f(SelShape<8, 8, 4, 32>{});
+    if (N <= 128) return f(SelShape<8, 16, 4, 32>{});
+    return f(SelShape<16, 16, 4, 16>{});
+}
+
+template <typename IO, int SL>
+cudaError_t step_rows_t(const SelArgs& a, cudaStream_t s) {
+    const int tiles = sel_tiles(a.D, a.G, 32);
+    const unsigned x = (unsigned)((tiles + 3) / 4);
+    // several sequences a warp where there are enough of them
+    if ((long long)tiles * a.batch >= 148 * 64) {
+        sel_step_rows_kernel<IO, SL, 4><<<dim3(x, (a.batch + 3) / 4), 128, 0, s>>>(a);
+    } else {
+        sel_step_rows_kernel<IO, SL, 1><<<dim3(x, a.batch), 128, 0, s>>>(a);
+    }
+    return cudaGetLastError();
 }
 
 template <typename IO, bool WIDE>
 cudaError_t step_t(const SelArgs& a, cudaStream_t s) {
+    if (WIDE && a.step_rows) {
+        if (a.N == 4) return step_rows_t<IO, 1>(a, s);
+        if (a.N == 8) return step_rows_t<IO, 2>(a, s);
+        if (a.N == 16) return step_rows_t<IO, 4>(a, s);
+        if (a.N == 32) return step_rows_t<IO, 8>(a, s);
+    }
     const long long cells = (long long)a.batch * a.D;
     auto blocks = [&](int sl) { return (unsigned)((cells * sl + 127) / 128); };
     if (a.N <= 4)
@@ -228,22 +457,22 @@ cudaError_t step_t(const SelArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// Channels of a forward block, by the number of states (fwd_by_n).
+// Channels of a forward block.
 static int sel_fwd_channels(int N) {
-    int s = 1;
-    while (s < 16 && s * 8 < N) s *= 2;
-    return 128 / s;
+    return fwd_shape(N, [](auto sh) { return 2 * decltype(sh)::CB; });
 }
 
-// Segments: none while the blocks of one pass over the channels give every SM sub-partition a
-// warp to itself; else as many as bring four warps to each, of at least four tiles of tokens.
+// Segments.  A segmented call computes every decay twice (measured 1.75 times the work), so it
+// pays where the blocks of one pass would leave more than half of the GPU idle: then as many
+// segments as fill it once (seven blocks an SM), of at least two tiles of tokens.
 int sel_fwd_segments(int batch, int T, int D, int G, int N, int* seg) {
     const int tiles = (T + kSelTile - 1) / kSelTile;
     const long long blocks = (long long)batch * sel_tiles(D, G, sel_fwd_channels(N));
     int n = 1;
-    if (blocks < 148 && tiles >= 8) {
-        n = (int)((148 * 4 + blocks - 1) / blocks);
-        if (n > tiles / 4) n = tiles / 4;
+    if (blocks <= 148 * 3) {
+        n = (int)(148 * 7 / blocks);
+        if (n > tiles / 2) n = tiles / 2;
+        if (n < 1) n = 1;
     }
     const int per = (tiles + n - 1) / n;
     *seg = per * kSelTile;
@@ -257,7 +486,10 @@ size_t sel_fwd_workspace(int batch, int T, int D, int G, int N) {
 }
 
 cudaError_t launch_sel_fwd(const SelArgs& a, int io_dtype, cudaStream_t s) {
-    return io_dtype == M3_BF16 ? fwd_by_n<__nv_bfloat16>(a, s) : fwd_by_n<float>(a, s);
+    return fwd_shape(a.N, [&](auto sh) {
+        using SH = decltype(sh);
+        return io_dtype == M3_BF16 ? fwd_t<__nv_bfloat16, SH>(a, s) : fwd_t<float, SH>(a, s);
+    });
 }
 
 cudaError_t launch_sel_step(const SelArgs& a, int io_dtype, cudaStream_t s) {

@@ -9,8 +9,9 @@
 
 namespace m3 {
 
-template <int NT_, int S_, int WARPS_, int L_ = kSelTile>
+template <int NT_, int S_, int WARPS_, int L_ = kSelTile, int GT_ = 1>
 struct SelShape {
+    static constexpr int GT = GT_;               // tokens whose decays are computed together
     static constexpr int NT = NT_, S = S_, WARPS = WARPS_;
     static constexpr int L = L_;                 // tokens staged together (S divides it)
     static constexpr int CW = 32 / S;            // channels of a warp
@@ -47,6 +48,67 @@ __host__ __device__ inline int sel_tiles(int D, int G, int CB) { return (D / G +
 __device__ __forceinline__ float sel_delta(float dt, float bias, bool softplus) {
     const float v = dt + bias;
     return softplus ? softplus_f(v) : v;
+}
+
+__device__ __forceinline__ f2 ex2_2(f2 v) {
+    float lo, hi;
+    unpack2(v, lo, hi);
+    return pack2(ex2(lo), ex2(hi));
+}
+
+// 2 M neighbouring floats of shared memory as pairs, in 16-byte reads where there are four
+template <int M>
+__device__ __forceinline__ void load_pairs(f2 (&v)[M], const float* p) {
+    if constexpr (M == 1) {
+        v[0] = *reinterpret_cast<const f2*>(p);
+    } else {
+#pragma unroll
+        for (int i = 0; i < M / 2; i++) {
+            const ulonglong2 q = reinterpret_cast<const ulonglong2*>(p)[i];
+            v[2 * i] = q.x;
+            v[2 * i + 1] = q.y;
+        }
+    }
+}
+
+// ------------------------------------------------------------------ asynchronous tiles
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool on) {
+    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    const int bytes = on ? 16 : 0;      // the rest of the 16 bytes is written as zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Rows t0 .. t0 + L - 1 of an activation, `width` values of each from `off` on, into sm[L][W]
+// as io values; rows at or past `end` and values past `width` read zero.  WIDE: 16-byte
+// asynchronous copies (rows on 16 bytes, width a multiple of 16 bytes); otherwise the values
+// are loaded and stored one by one.
+template <typename IO, bool WIDE, int L, int W, int THREADS>
+__device__ __forceinline__ void stage_rows(IO* sm, const View& v, int b, long long off, int t0,
+                                           int end, int width) {
+    const IO* p = static_cast<const IO*>(v.p) + b * v.bs + off;
+    if constexpr (WIDE) {
+        constexpr int V = 16 / sizeof(IO), PER = W / V;
+#pragma unroll
+        for (int i = threadIdx.x; i < L * PER; i += THREADS) {
+            const int u = i / PER, k = (i % PER) * V;
+            const bool on = t0 + u < end && k < width;
+            cp_async16(sm + u * W + k, on ? p + (t0 + u) * v.ts + k : p, on);
+        }
+    } else {
+#pragma unroll 8
+        for (int i = threadIdx.x; i < L * W; i += THREADS) {
+            const int u = i / W, k = i % W;
+            IO q = from_f<IO>(0.f);
+            if (t0 + u < end && k < width) q = p[(t0 + u) * v.ts + k];
+            sm[i] = q;
+        }
+    }
 }
 
 // B and C of tokens t0 .. t0 + L - 1 as floats in sm[L][2][NP]; tokens at or past `end` and
