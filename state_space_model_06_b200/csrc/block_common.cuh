@@ -19,14 +19,6 @@ __device__ __forceinline__ int tokens_of(const int32_t* seqlens, int b, int T) {
     return seqlens ? min(max(seqlens[b], 0), T) : T;
 }
 
-// Logistic function.  bf16 results round at 2^-9 (relative), so they take the hardware exp2
-// and reciprocal (a few 2^-22); fp32 results take expf and a rounded division.
-template <typename IO>
-__device__ __forceinline__ float sigmoid_f(float v) {
-    if constexpr (sizeof(IO) == 2) return __fdividef(1.f, 1.f + __expf(-v));
-    return 1.f / (1.f + expf(-v));
-}
-
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -36,6 +28,20 @@ __device__ __forceinline__ float ex2(float v) {
     return r;
 }
 
+__device__ __forceinline__ float rcp(float v) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// Logistic function.  bf16 results round at 2^-9 (relative), so they take the hardware exp2
+// and reciprocal (a few 2^-22); fp32 results take expf and a rounded division.
+template <typename IO>
+__device__ __forceinline__ float sigmoid_f(float v) {
+    if constexpr (sizeof(IO) == 2) return rcp(1.f + ex2(-kLog2e * v));
+    return 1.f / (1.f + expf(-v));
+}
+
 // Softplus: max(v, 0) + log(1 + u), u = e^-|v| in (0, 1].  The step multiplies every exponent of
 // the recurrence, so it is computed to fp32 rounding for every io type.  With s = u / (2 + u) in
 // (0, 1/3], log(1 + u) = 2 atanh(s) = 2 s (1 + s^2/3 + s^4/5 + ..): the four coefficients are a
@@ -43,7 +49,7 @@ __device__ __forceinline__ float ex2(float v) {
 // log(1 + u) from a rounded 1 + u is not.
 __device__ __forceinline__ float softplus_f(float v) {
     const float u = ex2(-fabsf(v) * kLog2e);
-    const float s = __fdividef(u, 2.f + u), q = s * s;
+    const float s = u * rcp(2.f + u), q = s * s;
     float r = 0.1400599330663681f;
     r = fmaf(r, q, 0.1400090307f);
     r = fmaf(r, q, 0.2001076341f);
@@ -79,6 +85,29 @@ __device__ __forceinline__ f2 add2(f2 a, f2 b) {
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
+// ------------------------------------------------------------------ asynchronous copies
+// Global to shared memory, without a register in between.  16 bytes (`on` false: zeros).
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool on) {
+    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    const int bytes = on ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(bytes)
+                 : "memory");
+}
+// N = 8 or 16 bytes.
+template <int N>
+__device__ __forceinline__ void cp_async(void* dst, const void* src) {
+    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    if constexpr (N == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(d), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // V consecutive io values as floats.  WIDE: one aligned vector access of V * sizeof(IO) bytes
 // (8 or 16, or 32 as two); otherwise element by element, the first n of them (the rest read 0
 // and are not written).

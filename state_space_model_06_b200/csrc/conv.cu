@@ -71,10 +71,16 @@ __device__ __forceinline__ void load_filter(const ConvArgs& a, int c0, int n, f2
 }
 
 template <typename IO>
-__device__ __forceinline__ f2 silu2(f2 v) {
+__device__ __forceinline__ f2 sigmoid2(f2 v) {
     float lo, hi;
-    unpack2(v, lo, hi);
-    return pack2(lo * sigmoid_f<IO>(lo), hi * sigmoid_f<IO>(hi));
+    if constexpr (sizeof(IO) == 2) {
+        unpack2(mul2(v, pack2(-kLog2e, -kLog2e)), lo, hi);
+        unpack2(add2(pack2(ex2(lo), ex2(hi)), pack2(1.f, 1.f)), lo, hi);
+        return pack2(rcp(lo), rcp(hi));
+    } else {
+        unpack2(v, lo, hi);
+        return pack2(sigmoid_f<IO>(lo), sigmoid_f<IO>(hi));
+    }
 }
 
 // The tokens before t0 into win[0 .. W-2].
@@ -92,10 +98,69 @@ __device__ __forceinline__ void load_window(const ConvArgs& a, const IO* x, long
     }
 }
 
+// A thread's coming tokens: R tensors, groups of U tokens, D groups on their way.  With wide rows
+// they come by asynchronous copies into places that the thread alone reads, so there is nothing
+// to wait for but its own copies; loads into registers held up to 3.5 TB/s (the prompt case:
+// 152 us), as a thread's registers hold only a few tokens and its loads share few scoreboards.
+template <typename IO, int R, int D, bool WIDE>
+struct Ahead {
+    static constexpr int U = 4;
+    const IO* p[R];
+    long long ts[R];
+    Quad<IO>* sm;      // [D][R][U][blockDim]
+    int n, left, slot;
+    __device__ __forceinline__ void start(int groups) {
+        left = groups;
+        slot = 0;
+        if constexpr (WIDE)
+#pragma unroll
+            for (int d = 0; d < D - 1; d++) ask(d);
+    }
+    __device__ __forceinline__ Quad<IO>* at(int d, int r, int u) {
+        return sm + ((d * R + r) * U + u) * 128 + threadIdx.x;
+    }
+    __device__ __forceinline__ void ask(int d) {
+        if (left > 0) {
+            left--;
+#pragma unroll
+            for (int r = 0; r < R; r++)
+#pragma unroll
+                for (int u = 0; u < U; u++) {
+                    cp_async<V * (int)sizeof(IO)>(at(d, r, u), p[r]);
+                    p[r] += ts[r];
+                }
+        }
+        cp_async_commit();
+    }
+    // The next group's values.
+    __device__ __forceinline__ void take(Quad<IO> (&q)[R][U]) {
+        if constexpr (WIDE) {
+            cp_async_wait<D - 2>();
+#pragma unroll
+            for (int r = 0; r < R; r++)
+#pragma unroll
+                for (int u = 0; u < U; u++) q[r][u] = *at(slot, r, u);
+            ask(slot == 0 ? D - 1 : slot - 1);      // the place of the group before
+            slot = slot == D - 1 ? 0 : slot + 1;
+        } else {
+#pragma unroll
+            for (int r = 0; r < R; r++)
+#pragma unroll
+                for (int u = 0; u < U; u++, p[r] += ts[r]) q[r][u] = load_quad<IO, WIDE>(p[r], n);
+        }
+    }
+    // One token more, behind the groups (p points at it once every group has been asked for).
+    __device__ __forceinline__ Quad<IO> one(int r) {
+        const Quad<IO> q = load_quad<IO, WIDE>(p[r], n);
+        p[r] += ts[r];
+        return q;
+    }
+};
+
 // ------------------------------------------------------------------ forward
 
 template <typename IO, int W, bool WIDE>
-__global__ void __launch_bounds__(128) conv_fwd_kernel(const ConvArgs a) {
+__global__ void __launch_bounds__(128, W <= 4 ? 7 : 4) conv_fwd_kernel(const ConvArgs a) {
     const int c0 = (blockIdx.y * blockDim.x + threadIdx.x) * V;
     if (c0 >= a.C) return;
     const int n = min(V, a.C - c0);
@@ -107,41 +172,43 @@ __global__ void __launch_bounds__(128) conv_fwd_kernel(const ConvArgs a) {
     const IO* x = static_cast<const IO*>(a.x.p) + b * a.x.bs + c0;
     IO* y = static_cast<IO*>(a.y.p) + b * a.y.bs + c0;
     IO* st = static_cast<IO*>(a.state) + (long long)b * (W - 1) * a.C + c0;
-    const int te = min(t1, len);
-    constexpr int U = 32 / (int)sizeof(IO) / 2;      // tokens on their way while U others are worked on
-    Quad<IO> next[U];
-    if (t0 < te)
-#pragma unroll
-        for (int u = 0; u < U; u++) next[u] = load_quad<IO, WIDE>(x + min(t0 + u, te - 1) * xts, n);
+    const int te = max(min(t1, len), t0);
+    using In = Ahead<IO, 1, 4, WIDE>;
+    constexpr int U = In::U;
+    __shared__ Quad<IO> sm[WIDE ? 4 * U * 128 : 1];
+    In in{{x + t0 * xts}, {xts}, sm, n};
+    const int groups = (te - t0) / U;
+    in.start(groups);
+    IO* py = y + t0 * yts;
 
     f2 w[W][2], bias[2], win[W][2];      // win[j] holds u_{t-W+1+j}
     load_filter<W, WIDE>(a, c0, n, w, bias);
     load_window<IO, W, WIDE>(a, x, xts, st, t0, len, n, win);
-    for (int t = t0; t < te; t += U) {
-        Quad<IO> cur[U];
+    auto token = [&](const Quad<IO>& q) {
+        f2 s[2];
+        widen(win[W - 1], q);
 #pragma unroll
-        for (int u = 0; u < U; u++) cur[u] = next[u];
-        if (t + U < te)
+        for (int i = 0; i < 2; i++) {
+            s[i] = bias[i];
 #pragma unroll
-            for (int u = 0; u < U; u++) next[u] = load_quad<IO, WIDE>(x + min(t + U + u, te - 1) * xts, n);
+            for (int k = 0; k < W; k++) s[i] = fma2(w[k][i], win[k][i], s[i]);
+            if (a.silu) s[i] = mul2(s[i], sigmoid2<IO>(s[i]));
 #pragma unroll
-        for (int u = 0; u < U; u++) {
-            f2 s[2];
-            widen(win[W - 1], cur[u]);
-#pragma unroll
-            for (int i = 0; i < 2; i++) {
-                s[i] = bias[i];
-#pragma unroll
-                for (int k = 0; k < W; k++) s[i] = fma2(w[k][i], win[k][i], s[i]);
-                if (a.silu) s[i] = silu2<IO>(s[i]);
-#pragma unroll
-                for (int k = 0; k < W - 1; k++) win[k][i] = win[k + 1][i];
-            }
-            if (t + u < te) store_quad<IO, WIDE>(s, y + (t + u) * yts, n);
+            for (int k = 0; k < W - 1; k++) win[k][i] = win[k + 1][i];
         }
+        store_quad<IO, WIDE>(s, py, n);
+        py += yts;
+    };
+    for (int g = 0; g < groups; g++) {
+        Quad<IO> q[1][U];
+        in.take(q);
+#pragma unroll
+        for (int u = 0; u < U; u++) token(q[0][u]);
     }
+    for (int t = t0 + groups * U; t < te; t++) token(in.one(0));
+    cp_async_wait<0>();
     const f2 zero[2] = {0, 0};
-    for (int t = max(t0, te); t < t1; t++) store_quad<IO, WIDE>(zero, y + t * yts, n);
+    for (int t = te; t < t1; t++) store_quad<IO, WIDE>(zero, y + t * yts, n);
 
     // The first run alone reads the state, so it also writes the new one: the last W - 1
     // tokens of [state | x], oldest first (place j is u_{len-W+1+j}; each source is at or behind
@@ -187,8 +254,8 @@ __global__ void __launch_bounds__(64) conv_step_kernel(const ConvArgs a) {
         s[1] = fma2(w[k][1], u[1], s[1]);
     }
     if (a.silu) {
-        s[0] = silu2<IO>(s[0]);
-        s[1] = silu2<IO>(s[1]);
+        s[0] = mul2(s[0], sigmoid2<IO>(s[0]));
+        s[1] = mul2(s[1], sigmoid2<IO>(s[1]));
     }
 #pragma unroll
     for (int j = 0; j < W - 1; j++) {
@@ -212,7 +279,7 @@ __global__ void __launch_bounds__(64) conv_step_kernel(const ConvArgs a) {
 // covers s = -(W-1) .. -1, the gradients of the carried tokens.
 
 template <typename IO, int W, bool WIDE>
-__global__ void __launch_bounds__(128) conv_bwd_kernel(const ConvArgs a) {
+__global__ void __launch_bounds__(128, W <= 4 ? 4 : 2) conv_bwd_kernel(const ConvArgs a) {
     const int c0 = (blockIdx.y * blockDim.x + threadIdx.x) * V;
     if (c0 >= a.C) return;
     const int n = min(V, a.C - c0);
@@ -227,17 +294,15 @@ __global__ void __launch_bounds__(128) conv_bwd_kernel(const ConvArgs a) {
     const IO* st = static_cast<const IO*>(a.state) + (long long)b * (W - 1) * a.C + c0;
 
     // the tokens that are looked at: this run's, and W - 1 behind it that only finish its dx
-    const int te = min(t1 + W - 1, len), last = t1 + W - 1;
-    constexpr int U = 4;
-    Quad<IO> nx[U], ng[U];
-    auto request = [&](int t) {
-#pragma unroll
-        for (int u = 0; u < U; u++) {
-            nx[u] = load_quad<IO, WIDE>(x + min(t + u, te - 1) * xts, n);
-            ng[u] = load_quad<IO, WIDE>(dy + min(t + u, te - 1) * gts, n);
-        }
-    };
-    if (t0 < te) request(t0);
+    const int te = max(min(t1 + W - 1, len), t0), last = t1 + W - 1;
+    constexpr int D = sizeof(IO) == 2 ? 4 : 3;
+    using In = Ahead<IO, 2, D, WIDE>;
+    constexpr int U = In::U;
+    __shared__ Quad<IO> sm[WIDE ? D * 2 * U * 128 : 1];
+    In in{{x + t0 * xts, dy + t0 * gts}, {xts, gts}, sm, n};
+    const int groups = max(min(t1, len) - t0, 0) / U;      // whole groups of the run's own tokens
+    in.start(groups);
+    IO* pd = dx + (t0 - (W - 1)) * dts;
     f2 w[W][2], bias[2], win[W][2], dw[W][2], acc[W][2], db[2] = {0, 0};
     load_filter<W, WIDE>(a, c0, n, w, bias);
     load_window<IO, W, WIDE>(a, x, xts, st, t0, len, n, win);
@@ -246,75 +311,75 @@ __global__ void __launch_bounds__(128) conv_bwd_kernel(const ConvArgs a) {
 #pragma unroll
         for (int i = 0; i < 2; i++) dw[k][i] = acc[k][i] = 0;   // acc[j]: dx_{t-W+1+j} so far
 
-    for (int t = t0; t < last; t += U) {
-        Quad<IO> cx[U], cg[U];
-#pragma unroll
-        for (int u = 0; u < U; u++) {
-            cx[u] = nx[u];
-            cg[u] = ng[u];
-        }
-        if (t + U < te) request(t + U);
-#pragma unroll
-        for (int u = 0; u < U; u++) {
-            if (t + u < last) {
-                f2 g[2] = {0, 0};
-                win[W - 1][0] = win[W - 1][1] = 0;
-                if (t + u < te) {      // past the length nothing is looked at
-                    widen(win[W - 1], cx[u]);
-                    widen(g, cg[u]);
-                    if (a.silu) {
-#pragma unroll
-                        for (int i = 0; i < 2; i++) {
-                            f2 s = bias[i];
-#pragma unroll
-                            for (int k = 0; k < W; k++) s = fma2(w[k][i], win[k][i], s);
-                            float v[2], d[2];
-                            unpack2(s, v[0], v[1]);
-#pragma unroll
-                            for (int j = 0; j < 2; j++) {
-                                const float sg = sigmoid_f<IO>(v[j]);
-                                d[j] = fmaf(v[j] * sg, 1.f - sg, sg);
-                            }
-                            g[i] = mul2(g[i], pack2(d[0], d[1]));
-                        }
-                    }
-                }
-                const bool mine = t + u < t1;
+    // inside: the token is inside the sequence; mine: it is one of the run's own
+    auto token = [&](const Quad<IO>& qx, const Quad<IO>& qg, int t, bool inside, bool mine) {
+        f2 g[2] = {0, 0};
+        win[W - 1][0] = win[W - 1][1] = 0;
+        if (inside) {
+            widen(win[W - 1], qx);
+            widen(g, qg);
+            if (a.silu) {
 #pragma unroll
                 for (int i = 0; i < 2; i++) {
-                    const f2 own = mine ? g[i] : 0;
-                    db[i] = add2(db[i], own);
+                    f2 s = bias[i];
 #pragma unroll
-                    for (int k = 0; k < W; k++) {
-                        dw[k][i] = fma2(own, win[k][i], dw[k][i]);
-                        acc[k][i] = fma2(w[k][i], g[i], acc[k][i]);
-                    }
-                }
-                // acc[0] is complete: the gradient of token t + u - W + 1
-                const int s = t + u - (W - 1);
-                if (s >= t0) {
-                    store_quad<IO, WIDE>(acc[0], dx + s * dts, n);
-                } else if (s < 0 && a.dstate) {      // a carried token
-                    float v[V];
-                    unpack2(acc[0][0], v[0], v[1]);
-                    unpack2(acc[0][1], v[2], v[3]);
-                    float* o = a.dstate + ((long long)b * (W - 1) + (s + W - 1)) * a.C + c0;
-#pragma unroll
-                    for (int i = 0; i < V; i++)
-                        if (i < n) o[i] = v[i];
-                }
-#pragma unroll
-                for (int i = 0; i < 2; i++) {
-#pragma unroll
-                    for (int k = 0; k < W - 1; k++) {
-                        win[k][i] = win[k + 1][i];
-                        acc[k][i] = acc[k + 1][i];
-                    }
-                    acc[W - 1][i] = 0;
+                    for (int k = 0; k < W; k++) s = fma2(w[k][i], win[k][i], s);
+                    // act' = sg + s sg (1 - sg)
+                    const f2 sg = sigmoid2<IO>(s), m = fma2(sg, pack2(-1.f, -1.f), pack2(1.f, 1.f));
+                    g[i] = mul2(g[i], fma2(mul2(s, sg), m, sg));
                 }
             }
         }
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            const f2 own = mine ? g[i] : 0;
+            db[i] = add2(db[i], own);
+#pragma unroll
+            for (int k = 0; k < W; k++) {
+                dw[k][i] = fma2(own, win[k][i], dw[k][i]);
+                acc[k][i] = fma2(w[k][i], g[i], acc[k][i]);
+            }
+        }
+        // acc[0] is complete: the gradient of token t - W + 1
+        const int s = t - (W - 1);
+        if (s >= t0) {
+            store_quad<IO, WIDE>(acc[0], pd, n);
+        } else if (s < 0 && a.dstate) {      // a carried token
+            float v[V];
+            unpack2(acc[0][0], v[0], v[1]);
+            unpack2(acc[0][1], v[2], v[3]);
+            float* o = a.dstate + ((long long)b * (W - 1) + (s + W - 1)) * a.C + c0;
+#pragma unroll
+            for (int i = 0; i < V; i++)
+                if (i < n) o[i] = v[i];
+        }
+        pd += dts;
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+#pragma unroll
+            for (int k = 0; k < W - 1; k++) {
+                win[k][i] = win[k + 1][i];
+                acc[k][i] = acc[k + 1][i];
+            }
+            acc[W - 1][i] = 0;
+        }
+    };
+    for (int k = 0; k < groups; k++) {
+        Quad<IO> q[2][U];
+        in.take(q);
+#pragma unroll
+        for (int u = 0; u < U; u++) token(q[0][u], q[1][u], t0 + k * U + u, true, true);
     }
+    for (int t = t0 + groups * U; t < last; t++) {
+        Quad<IO> qx, qg;
+        const bool inside = t < te;
+        if (inside) {
+            qx = in.one(0);
+            qg = in.one(1);
+        }
+        token(qx, qg, t, inside, t < t1);
+    }
+    cp_async_wait<0>();
     // shares of this run: [b * nseg + seg][W + 1][C]
     float* part = a.part + (long long)blockIdx.x * (W + 1) * a.C + c0;
 #pragma unroll

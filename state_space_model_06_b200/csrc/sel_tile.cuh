@@ -72,18 +72,6 @@ __device__ __forceinline__ void load_pairs(f2 (&v)[M], const float* p) {
 }
 
 // ------------------------------------------------------------------ asynchronous tiles
-__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool on) {
-    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
-    const int bytes = on ? 16 : 0;      // the rest of the 16 bytes is written as zeros
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(bytes)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Rows t0 .. t0 + L - 1 of an activation, `width` values of each from `off` on, into sm[L][W]
 // as io values; rows at or past `end` and values past `width` read zero.  WIDE: 16-byte
 // asynchronous copies (rows on 16 bytes, width a multiple of 16 bytes); otherwise the values
