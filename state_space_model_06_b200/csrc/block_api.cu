@@ -351,7 +351,7 @@ m3_status m3_sel_bwd_workspace_bytes(const m3_sel_dims* d, int32_t T, size_t* by
     SelArgs a;
     std::memset(&a, 0, sizeof(a));
     a.batch = d->batch; a.T = T; a.D = d->channels; a.G = d->ngroups; a.N = d->dstate;
-    const size_t n = sel_bwd_plan(&a, d->io_dtype, nullptr);
+    const size_t n = sel_bwd_plan(&a, nullptr);
     *bytes = n < 256 ? 256 : n;
     return M3_OK;
 }
@@ -392,7 +392,7 @@ m3_status m3_sel_bwd(const m3_sel_dims* d, int32_t T, const m3_sel_inputs* in, c
         return st;
     SelArgs a;
     sel_args(&a, d, T, in, h0, flags);
-    const size_t need = sel_bwd_plan(&a, d->io_dtype, static_cast<char*>(ws));
+    const size_t need = sel_bwd_plan(&a, static_cast<char*>(ws));
     if (!ws || !at_least(ws, 256) || ws_bytes < need) return M3_ERR_WORKSPACE;
     if (!sel_grid_ok(a)) return M3_ERR_UNSUPPORTED;
     a.dy = view(*dy);
@@ -401,6 +401,8 @@ m3_status m3_sel_bwd(const m3_sel_dims* d, int32_t T, const m3_sel_inputs* in, c
     set_out(a.dB, gr->dB);
     set_out(a.dC, gr->dC);
     set_out(a.dz, gr->dz);
+    a.wide = sel_wide(d, g, in) && wide_rows(*dy, g) && wide_rows(gr->dx, g) &&
+             wide_rows(gr->ddt, g) && (!in->z.ptr || wide_rows(gr->dz, g));
     a.dhT = dhT;
     a.dA = gr->dA;
     a.dD = in->D ? gr->dD : nullptr;

@@ -45,14 +45,18 @@ struct SelArgs {
     const float* dhT;
     float *dA, *dD, *ddt_bias, *dh;
     // workspace
-    float* hseg;           // [b][nseg][D][N]: each segment's own end state, then its entry state
-    float* gseg;           // [b][nseg][D][N]: backward: own entry adjoint, then the leaving adjoint
-    float* dsum;           // [b][nseg][D]: sum of delta over the segment
-    float* pBC;            // [tiles][b][T][2 N]: backward: shares of dB and dC
+    float* hseg;           // [b][nseg][D][N]: forward: each segment's own end state, then its entry
+                           // state; backward: its entry state
+    float* dsum;           // forward [b][nseg][D]: sum of delta over the segment; backward
+                           // [b][ntile][D]: from the segment's start through the tile
+    float* hloc;           // [b][ntile][D][N]: backward: the segment's own state after the tile
+    float* gseg;           // [b][nseg][D][N]: own entry adjoint, then the leaving adjoint
+    float* pBC;            // [b][T][channel blocks][2][states padded]: shares of dB and dC
     float* pA;             // [b * nseg][D][N]
     float* pD;             // [b * nseg][2][D]: dD, ddt_bias
     int batch, T, D, G, N;
     int seg, nseg;         // tokens per segment (a multiple of the tile), segments
+    int tile, ntile;       // backward: tokens per tile, tiles
     bool softplus, wide, step_rows;
 };
 // Tokens of one staged tile: segments are multiples of it.
@@ -62,7 +66,7 @@ size_t sel_fwd_workspace(int batch, int T, int D, int G, int N);
 cudaError_t launch_sel_fwd(const SelArgs& a, int io_dtype, cudaStream_t s);
 cudaError_t launch_sel_step(const SelArgs& a, int io_dtype, cudaStream_t s);
 // Fills in seg, nseg and the workspace pointers (relative to a null workspace: sizes alone).
-size_t sel_bwd_plan(SelArgs* a, int io_dtype, char* ws);
+size_t sel_bwd_plan(SelArgs* a, char* ws);
 cudaError_t launch_sel_bwd(const SelArgs& a, int io_dtype, cudaStream_t s);
 
 // ------------------------------------------------------------------ norm

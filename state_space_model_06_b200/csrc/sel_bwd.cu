@@ -5,14 +5,22 @@
 // and each token gives
 //   dC_t[n] = sum_c h_t e_t;   dB_t[n] = sum_c lam_t delta_t x_t;   dx_t = delta_t sum_n lam_t B_t + D e_t;
 //   ddelta_t = x_t sum_n lam_t B_t + sum_n A lam_t a_t h_{t-1};     dA = sum_t delta_t lam_t a_t h_{t-1}.
-// Both recurrences are affine in the state that enters a segment, so every segment of the
-// sequence works by itself once its entry state and its leaving adjoint are known:
-//   1. sel_bwd_local_kernel: each segment's own end state (from 0) and own entry adjoint (to 0);
+// Both recurrences are affine in what enters a segment, so every segment of the sequence works by
+// itself once its entry state and its leaving adjoint are known:
+//   1. sel_bwd_local_kernel: each segment's own states at the ends of its tiles (from a zero entry)
+//      and its own entry adjoint (from a zero leaving one);
 //   2. sel_bwd_chain_kernel: entry states forward and leaving adjoints backward over segments;
-//   3. sel_bwd_kernel: the segment again, K tokens at a time from the last: the K states and
-//      decays of a piece are recomputed into registers from a state kept in shared memory, then
-//      walked backward;
+//   3. sel_bwd_kernel: the segment's tiles again, from the last.  Within a tile the states before
+//      every K tokens go to shared memory; then, K tokens at a time from the last, states and
+//      decays are recomputed into registers and walked backward;
 //   4. the shares of the sums over channel blocks and over segments are added in a fixed order.
+// A tile's entry state is its segment's entry state decayed to the tile, plus the own state of
+// step 1, so only whole segments are chained.
+//
+// As in the forward kernel a lane holds NT states of two neighbouring channels, as packed pairs
+// of states: the sums over channels (dB, dC) then cross half as many lanes, and they are what
+// would cost most (a value summed over 8 lanes takes 7/8 of a shuffle and four times that in
+// other instructions).
 #include "block_internal.h"
 #include "sel_tile.cuh"
 
@@ -21,169 +29,213 @@ namespace m3 {
 namespace {
 
 template <int NT_, int S_, int WARPS_, int L_, int K_>
-struct BwdShape : SelShape<NT_, S_, WARPS_, L_> {
-    using Base = SelShape<NT_, S_, WARPS_, L_>;
-    static constexpr int L = L_, K = K_;      // tokens of a segment, of a piece
+struct BwdShape {
+    static constexpr int NT = NT_, S = S_, WARPS = WARPS_;
+    static constexpr int L = L_, K = K_;         // tokens of a tile, of a piece
+    static constexpr int CW = 32 / S;            // pairs of channels of a warp
+    static constexpr int PB = CW * WARPS;        // pairs of channels of a block
+    static constexpr int CB = 2 * PB;            // channels of a block
+    static constexpr int NP = NT * S;            // states, padded
+    static constexpr int THREADS = 32 * WARPS;
+    static constexpr int MIN_BLOCKS = NT * K <= 16 ? 512 / THREADS : 1;   // 128 registers a thread
+    static constexpr int LOCAL_BLOCKS = NT == 4 ? 768 / THREADS : 1;      // 80 registers
     // shared memory, in floats
-    static constexpr int O_BC = 0;                                      // [L][2][NP]
-    static constexpr int O_DELTA = O_BC + L * 2 * Base::NP;             // [L][CB]
-    static constexpr int O_DX = O_DELTA + L * Base::CB;                 // [L][CB] delta x
-    static constexpr int O_E = O_DX + L * Base::CB;                     // [L][CB]
-    static constexpr int O_CK = O_E + L * Base::CB;                     // [L / K][CB][NP]
-    static constexpr int O_RED = O_CK + L / K * Base::CB * Base::NP;    // [WARPS][K][2 NP]
+    static constexpr int O_BC = 0;                              // [L][2][NP]
+    static constexpr int O_DD = O_BC + L * 2 * NP;              // [L][PB] float4: delta, delta x of two channels
+    static constexpr int O_E = O_DD + L * PB * 4;               // [L][PB] float2: e
+    static constexpr int O_CK = O_E + L * PB * 2;               // [L / K][CB][NP]
+    static constexpr int O_RED = O_CK + L / K * CB * NP;        // [WARPS][K][2 NP]
     static constexpr int LOCAL_BYTES = 4 * O_CK;
-    static constexpr int BYTES = 4 * (O_RED + Base::WARPS * K * 2 * Base::NP);
+    static constexpr int BYTES = 4 * (O_RED + WARPS * K * 2 * NP);
+    static_assert(BYTES <= 227 * 1024 && THREADS % PB == 0, "");
 };
 
-// delta, delta x and e = dy SiLU(z) of the segment's tokens (zero past the end), and B and C
-template <typename IO, typename SH>
-__device__ __forceinline__ void bwd_stage(const SelArgs& a, const SelPlace& p, int end, float* sm) {
-    constexpr int L = SH::L, CB = SH::CB;
+// Two neighbouring values of a row (`two` false: the second is not there).
+template <typename IO, bool WIDE>
+__device__ __forceinline__ float2 load_two(const IO* p, bool two) {
+    if constexpr (WIDE) return pair_of(p);
+    return make_float2(to_f(p[0]), two ? to_f(p[1]) : 0.f);
+}
+
+// delta, delta x and e = dy SiLU(z) of a tile's tokens (zero past the end), and B and C
+template <typename IO, typename SH, bool WIDE>
+__device__ __forceinline__ void bwd_stage(const SelArgs& a, const SelPlace& p, int t0, int end,
+                                          float* sm) {
+    constexpr int PB = SH::PB;
     const Rows<const IO> X{static_cast<const IO*>(a.x.p), a.x.bs, a.x.ts};
     const Rows<const IO> DT{static_cast<const IO*>(a.dt.p), a.dt.bs, a.dt.ts};
     const Rows<const IO> Z{static_cast<const IO*>(a.z.p), a.z.bs, a.z.ts};
     const Rows<const IO> DY{static_cast<const IO*>(a.dy.p), a.dy.bs, a.dy.ts};
-    sel_stage_bc<IO, SH::NP, L, SH::THREADS>(a, p, p.t0, end, sm + SH::O_BC);
+    sel_stage_bc<IO, SH::NP, SH::L, SH::THREADS>(a, p, t0, end, sm + SH::O_BC);
+    const int k = threadIdx.x % PB, c = p.c0 + 2 * k;
+    const bool one = 2 * k < p.nc, two = 2 * k + 1 < p.nc;
+    const float2 bias = make_float2(one && a.dt_bias ? a.dt_bias[c] : 0.f,
+                                    two && a.dt_bias ? a.dt_bias[c + 1] : 0.f);
 #pragma unroll 2
-    for (int i = threadIdx.x; i < L * CB; i += SH::THREADS) {
-        const int k = i % CB, t = p.t0 + i / CB;
-        float delta = 0.f, dx = 0.f, e = 0.f;
-        if (t < end && k < p.nc) {
-            const int c = p.c0 + k;
-            delta = sel_delta(to_f(DT.at(p.b, t)[c]), a.dt_bias ? a.dt_bias[c] : 0.f, a.softplus);
-            dx = delta * to_f(X.at(p.b, t)[c]);
-            e = to_f(DY.at(p.b, t)[c]);
+    for (int u = threadIdx.x / PB; u < SH::L; u += SH::THREADS / PB) {
+        const int t = t0 + u;
+        float2 delta = make_float2(0.f, 0.f), dx = delta, e = delta;
+        if (t < end && one) {
+            const float2 dt = load_two<IO, WIDE>(DT.at(p.b, t) + c, two);
+            const float2 x = load_two<IO, WIDE>(X.at(p.b, t) + c, two);
+            e = load_two<IO, WIDE>(DY.at(p.b, t) + c, two);
             if (a.z.p) {
-                const float z = to_f(Z.at(p.b, t)[c]);
-                e *= z * sigmoid_f<IO>(z);
+                const float2 z = load_two<IO, WIDE>(Z.at(p.b, t) + c, two);
+                e.x *= z.x * sigmoid_f<IO>(z.x);
+                e.y *= z.y * sigmoid_f<IO>(z.y);
             }
+            delta.x = sel_delta(dt.x, bias.x, a.softplus);
+            delta.y = two ? sel_delta(dt.y, bias.y, a.softplus) : 0.f;
+            dx.x = delta.x * x.x;
+            dx.y = delta.y * x.y;
         }
-        sm[SH::O_DELTA + i] = delta;
-        sm[SH::O_DX + i] = dx;
-        sm[SH::O_E + i] = e;
+        reinterpret_cast<float4*>(sm + SH::O_DD)[u * PB + k] = make_float4(delta.x, delta.y, dx.x, dx.y);
+        reinterpret_cast<float2*>(sm + SH::O_E)[u * PB + k] = e;
     }
 }
 
+// A lane's NT states (as pairs) of a [..][N] row; zero where there are none.
 template <int NT>
-__device__ __forceinline__ void load_states(float (&v)[NT], const float* p) {
+__device__ __forceinline__ void row_pairs(f2 (&v)[NT / 2], const float* p, bool live, int n0, int N,
+                                          float scale) {
 #pragma unroll
-    for (int q = 0; q < NT / 4; q++) {
-        const float4 f = reinterpret_cast<const float4*>(p)[q];
-        v[4 * q] = f.x; v[4 * q + 1] = f.y; v[4 * q + 2] = f.z; v[4 * q + 3] = f.w;
+    for (int i = 0; i < NT / 2; i++) {
+        float f[2];
+#pragma unroll
+        for (int j = 0; j < 2; j++)
+            f[j] = live && n0 + 2 * i + j < N ? p[n0 + 2 * i + j] * scale : 0.f;
+        v[i] = pack2(f[0], f[1]);
     }
 }
-
-template <typename IO, typename SH>
-__global__ void __launch_bounds__(SH::THREADS) sel_bwd_local_kernel(const SelArgs a) {
-    extern __shared__ __align__(16) float sm[];
-    constexpr int NT = SH::NT, CW = SH::CW, CB = SH::CB, NP = SH::NP;
-    const SelPlace p = sel_place(a, CB);
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    const int cl = wid * CW + lane % CW, s = lane / CW, c = p.c0 + cl;
-    const bool live = cl < p.nc;
-    const int end = min(p.t1, p.len);
-    bwd_stage<IO, SH>(a, p, end, sm);
-    float h[NT], g[NT], P[NT], A2[NT];
+template <int NT>
+__device__ __forceinline__ void store_pairs(const f2 (&v)[NT / 2], float* p, bool live, int n0, int N) {
 #pragma unroll
-    for (int i = 0; i < NT; i++) {
-        const int n = s * NT + i;
-        A2[i] = live && n < a.N ? a.A[(long long)c * a.N + n] * kLog2e : 0.f;
-        h[i] = g[i] = 0.f;
-        P[i] = 1.f;
+    for (int i = 0; i < NT / 2; i++) {
+        float f[2];
+        unpack2(v[i], f[0], f[1]);
+#pragma unroll
+        for (int j = 0; j < 2; j++)
+            if (live && n0 + 2 * i + j < N) p[n0 + 2 * i + j] = f[j];
     }
-    __syncthreads();
-    float total = 0.f;
-#pragma unroll 4
-    for (int u = 0; u < end - p.t0; u++) {
-        const float delta = sm[SH::O_DELTA + u * CB + cl], dx = sm[SH::O_DX + u * CB + cl],
-                    e = sm[SH::O_E + u * CB + cl];
-        float B[NT], C[NT];
-        load_states(B, sm + SH::O_BC + u * 2 * NP + s * NT);
-        load_states(C, sm + SH::O_BC + (u * 2 + 1) * NP + s * NT);
-        total += delta;
+}
+__device__ __forceinline__ float sum2(f2 v) {
+    float lo, hi;
+    unpack2(v, lo, hi);
+    return lo + hi;
+}
+
+template <typename IO, typename SH, bool WIDE>
+__global__ void __launch_bounds__(SH::THREADS, SH::LOCAL_BLOCKS) sel_bwd_local_kernel(const SelArgs a) {
+    extern __shared__ __align__(16) float sm[];
+    constexpr int NT = SH::NT, CW = SH::CW, PB = SH::PB, NP = SH::NP, L = SH::L;
+    const SelPlace p = sel_place(a, SH::CB);
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    const int pl = wid * CW + lane % CW, s = lane / CW, c = p.c0 + 2 * pl;
+    const int end = min(p.t1, p.len), tiles = a.seg / L;
+    f2 h[2][NT / 2], g[2][NT / 2], P[2][NT / 2], A2[2][NT / 2];
 #pragma unroll
-        for (int i = 0; i < NT; i++) {
-            const float d = ex2(delta * A2[i]);
-            h[i] = fmaf(d, h[i], dx * B[i]);
-            P[i] *= d;                      // decay from the entry through this token
-            g[i] = fmaf(P[i], C[i] * e, g[i]);
+    for (int q = 0; q < 2; q++) {
+        row_pairs<NT>(A2[q], a.A + (long long)(c + q) * a.N, 2 * pl + q < p.nc, s * NT, a.N, kLog2e);
+#pragma unroll
+        for (int i = 0; i < NT / 2; i++) {
+            h[q][i] = g[q][i] = 0;
+            P[q][i] = pack2(1.f, 1.f);
         }
     }
-    if (live) {
-        const long long row = (((long long)p.b * a.nseg + p.seg) * a.D + c) * a.N;
+    float total[2] = {0.f, 0.f};
+    for (int j = 0; j < tiles; j++) {
+        const int t0 = p.t0 + j * L;
+        const int count = min(L, end - t0);
+        if (count > 0) {
+            __syncthreads();
+            bwd_stage<IO, SH, WIDE>(a, p, t0, end, sm);
+            __syncthreads();
+        }
+#pragma unroll 2
+        for (int u = 0; u < count; u++) {
+            const float4 d = reinterpret_cast<const float4*>(sm + SH::O_DD)[u * PB + pl];
+            const float2 e = reinterpret_cast<const float2*>(sm + SH::O_E)[u * PB + pl];
+            const float dv[2] = {d.x, d.y}, xv[2] = {d.z, d.w}, ev[2] = {e.x, e.y};
+            f2 B[NT / 2], C[NT / 2];
+            load_pairs(B, sm + SH::O_BC + u * 2 * NP + s * NT);
+            load_pairs(C, sm + SH::O_BC + (u * 2 + 1) * NP + s * NT);
 #pragma unroll
-        for (int i = 0; i < NT; i++) {
-            const int n = s * NT + i;
-            if (n < a.N) {
-                a.hseg[row + n] = h[i];
-                a.gseg[row + n] = g[i];
+            for (int q = 0; q < 2; q++) {
+                const f2 delta = pack2(dv[q], dv[q]), dx = pack2(xv[q], xv[q]), eq = pack2(ev[q], ev[q]);
+                total[q] += dv[q];
+#pragma unroll
+                for (int i = 0; i < NT / 2; i++) {
+                    const f2 dec = ex2_2(mul2(delta, A2[q][i]));
+                    h[q][i] = fma2(dec, h[q][i], mul2(dx, B[i]));
+                    P[q][i] = mul2(P[q][i], dec);      // decay from the entry through this token
+                    g[q][i] = fma2(P[q][i], mul2(C[i], eq), g[q][i]);
+                }
             }
         }
-        if (s == 0) a.dsum[((long long)p.b * a.nseg + p.seg) * a.D + c] = total;
+        if (t0 < p.t1) {      // a tile of the sequence (the last segment may have fewer)
+            const long long k = (long long)p.b * a.ntile + p.seg * tiles + j;
+#pragma unroll
+            for (int q = 0; q < 2; q++) {
+                store_pairs<NT>(h[q], a.hloc + (k * a.D + c + q) * a.N, 2 * pl + q < p.nc, s * NT, a.N);
+                if (s == 0 && 2 * pl + q < p.nc) a.dsum[k * a.D + c + q] = total[q];
+            }
+        }
     }
+    const long long k = (long long)p.b * a.nseg + p.seg;
+#pragma unroll
+    for (int q = 0; q < 2; q++)
+        store_pairs<NT>(g[q], a.gseg + (k * a.D + c + q) * a.N, 2 * pl + q < p.nc, s * NT, a.N);
 }
 
-// Entry states over the segments in order, leaving adjoints over them in reverse; dh is what
-// leaves before the first.
-__global__ void __launch_bounds__(128) sel_bwd_chain_kernel(const SelArgs a) {
+// Entry states over the segments in order (the grid's first half), leaving adjoints over them in
+// reverse (its second half); dh is what leaves before the first.
+__global__ void __launch_bounds__(128) sel_bwd_chain_kernel(const SelArgs a, int blocks) {
     const long long per = (long long)a.D * a.N;
-    const long long i = blockIdx.x * 128ll + threadIdx.x;
+    const bool back = blockIdx.x >= blocks;
+    const long long i = (back ? blockIdx.x - blocks : blockIdx.x) * 128ll + threadIdx.x;
     if (i >= per * a.batch) return;
     const int b = (int)(i / per);
     const long long dn = i - b * per;
     const int d = (int)(dn / a.N);
     const float A2 = a.A[dn] * kLog2e;
-    float* hs = a.hseg + (long long)b * a.nseg * per + dn;
-    float* gs = a.gseg + (long long)b * a.nseg * per + dn;
-    const float* ds = a.dsum + (long long)b * a.nseg * a.D + d;
+    const int tiles = a.seg / a.tile;
+    // the last tile of segment k
+    auto tile_of = [&](int k) { return (long long)b * a.ntile + min((k + 1) * tiles, a.ntile) - 1; };
+    const float* ds = a.dsum + d;
+    float* out = (back ? a.gseg : a.hseg) + (long long)b * a.nseg * per + dn;
     constexpr int U = 8;          // segments requested together
-    float h = a.h[i];
+    float v = back ? (a.dhT ? a.dhT[i] : 0.f) : a.h[i];
     for (int k0 = 0; k0 < a.nseg; k0 += U) {
         float own[U], dec[U];
 #pragma unroll
         for (int u = 0; u < U; u++)
             if (k0 + u < a.nseg) {
-                own[u] = hs[(k0 + u) * per];
-                dec[u] = ds[(long long)(k0 + u) * a.D];
+                const int k = back ? a.nseg - 1 - (k0 + u) : k0 + u;
+                own[u] = back ? out[k * per] : a.hloc[tile_of(k) * per + dn];
+                dec[u] = ds[tile_of(k) * a.D];
             }
 #pragma unroll
         for (int u = 0; u < U; u++)
             if (k0 + u < a.nseg) {
-                hs[(k0 + u) * per] = h;
-                h = fmaf(ex2(A2 * dec[u]), h, own[u]);
+                const int k = back ? a.nseg - 1 - (k0 + u) : k0 + u;
+                out[k * per] = v;
+                v = fmaf(ex2(A2 * dec[u]), v, own[u]);
             }
     }
-    float g = a.dhT ? a.dhT[i] : 0.f;
-    for (int k0 = a.nseg - 1; k0 >= 0; k0 -= U) {
-        float own[U], dec[U];
-#pragma unroll
-        for (int u = 0; u < U; u++)
-            if (k0 - u >= 0) {
-                own[u] = gs[(k0 - u) * per];
-                dec[u] = ds[(long long)(k0 - u) * a.D];
-            }
-#pragma unroll
-        for (int u = 0; u < U; u++)
-            if (k0 - u >= 0) {
-                gs[(k0 - u) * per] = g;
-                g = fmaf(ex2(A2 * dec[u]), g, own[u]);
-            }
-    }
-    if (a.dh) a.dh[i] = g;
+    if (back && a.dh) a.dh[i] = v;
 }
 
-template <typename IO, typename SH>
-__global__ void __launch_bounds__(SH::THREADS) sel_bwd_kernel(const SelArgs a) {
+template <typename IO, typename SH, bool WIDE>
+__global__ void __launch_bounds__(SH::THREADS, SH::MIN_BLOCKS) sel_bwd_kernel(const SelArgs a) {
     extern __shared__ __align__(16) float sm[];
-    constexpr int NT = SH::NT, S = SH::S, CW = SH::CW, CB = SH::CB, NP = SH::NP, K = SH::K;
-    constexpr int WARPS = SH::WARPS;
+    constexpr int NT = SH::NT, S = SH::S, CW = SH::CW, PB = SH::PB, CB = SH::CB, NP = SH::NP;
+    constexpr int K = SH::K, L = SH::L, WARPS = SH::WARPS;
     const SelPlace p = sel_place(a, CB);
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    const int cl = wid * CW + lane % CW, s = lane / CW, c = p.c0 + cl;
-    const bool live = cl < p.nc;
+    const int pl = wid * CW + lane % CW, s = lane / CW, c = p.c0 + 2 * pl;
+    const int mine = min(max(p.nc - 2 * pl, 0), 2);      // channels of the pair that exist
     const int end = min(p.t1, p.len);
-    const int tile = blockIdx.x % sel_tiles(a.D, a.G, CB), tiles = sel_tiles(a.D, a.G, CB);
-    bwd_stage<IO, SH>(a, p, end, sm);
+    const int blk = blockIdx.x % sel_tiles(a.D, a.G, CB), blks = sel_tiles(a.D, a.G, CB);
 
     const Rows<const IO> X{static_cast<const IO*>(a.x.p), a.x.bs, a.x.ts};
     const Rows<const IO> DT{static_cast<const IO*>(a.dt.p), a.dt.bs, a.dt.ts};
@@ -193,130 +245,198 @@ __global__ void __launch_bounds__(SH::THREADS) sel_bwd_kernel(const SelArgs a) {
     const Rows<IO> DDT{static_cast<IO*>(a.ddt.p), a.ddt.bs, a.ddt.ts};
     const Rows<IO> DZ{static_cast<IO*>(a.dz.p), a.dz.bs, a.dz.ts};
 
-    float h[NT], lam[NT], A2[NT], dA[NT];
+    f2 lam[2][NT / 2], A2[2][NT / 2], dA[2][NT / 2];
+    float skip[2] = {0.f, 0.f}, bias[2] = {0.f, 0.f}, dD[2] = {0.f, 0.f}, dbias[2] = {0.f, 0.f};
     const long long row = (((long long)p.b * a.nseg + p.seg) * a.D + c) * a.N;
 #pragma unroll
-    for (int i = 0; i < NT; i++) {
-        const int n = s * NT + i;
-        const bool on = live && n < a.N;
-        A2[i] = on ? a.A[(long long)c * a.N + n] * kLog2e : 0.f;
-        h[i] = on ? a.hseg[row + n] : 0.f;
-        lam[i] = on ? a.gseg[row + n] : 0.f;
-        dA[i] = 0.f;
-    }
-    const float skip = live && a.Dskip ? a.Dskip[c] : 0.f;
-    const float bias = live && a.dt_bias ? a.dt_bias[c] : 0.f;
-    float dD = 0.f, dbias = 0.f;
-    __syncthreads();
-
-    const int count = end > p.t0 ? end - p.t0 : 0;
-    const int pieces = (count + K - 1) / K;
-    // the state before each piece (a thread reads back its own values only)
-    for (int j = 0; j < pieces; j++) {
-        float4* ck = reinterpret_cast<float4*>(sm + SH::O_CK + (j * CB + cl) * NP + s * NT);
+    for (int q = 0; q < 2; q++) {
+        row_pairs<NT>(A2[q], a.A + (long long)(c + q) * a.N, q < mine, s * NT, a.N, kLog2e);
+        row_pairs<NT>(lam[q], a.gseg + row + q * a.N, q < mine, s * NT, a.N, 1.f);
 #pragma unroll
-        for (int q = 0; q < NT / 4; q++)
-            ck[q] = make_float4(h[4 * q], h[4 * q + 1], h[4 * q + 2], h[4 * q + 3]);
-        if (j + 1 < pieces) {
+        for (int i = 0; i < NT / 2; i++) dA[q][i] = 0;
+        if (q < mine && a.Dskip) skip[q] = a.Dskip[c + q];
+        if (q < mine && a.dt_bias) bias[q] = a.dt_bias[c + q];
+    }
+
+    const int tiles = a.seg / L;
+    for (int jt = tiles - 1; jt >= 0; jt--) {
+        const int t0 = p.t0 + jt * L;
+        const int count = min(L, end - t0);
+        if (count <= 0) continue;
+        __syncthreads();
+        bwd_stage<IO, SH, WIDE>(a, p, t0, end, sm);
+        f2 h[2][NT / 2];
+#pragma unroll
+        for (int q = 0; q < 2; q++) {
+            row_pairs<NT>(h[q], a.hseg + row + q * a.N, q < mine, s * NT, a.N, 1.f);
+            if (jt > 0) {
+                // decayed from the segment's entry, plus the segment's own
+                const long long k = (long long)p.b * a.ntile + p.seg * tiles + jt - 1;
+                const float sum = q < mine ? a.dsum[k * a.D + c + q] : 0.f;
+                f2 own[NT / 2];
+                row_pairs<NT>(own, a.hloc + (k * a.D + c + q) * a.N, q < mine, s * NT, a.N, 1.f);
+#pragma unroll
+                for (int i = 0; i < NT / 2; i++)
+                    h[q][i] = fma2(ex2_2(mul2(pack2(sum, sum), A2[q][i])), h[q][i], own[i]);
+            }
+        }
+        __syncthreads();
+
+        const float4* dd = reinterpret_cast<const float4*>(sm + SH::O_DD) + pl;
+        const float2* ee = reinterpret_cast<const float2*>(sm + SH::O_E) + pl;
+        const int pieces = (count + K - 1) / K;
+        // the state before each piece (a thread reads back its own values only)
+        for (int j = 0; j < pieces; j++) {
+#pragma unroll
+            for (int q = 0; q < 2; q++) {
+                f2* ck = reinterpret_cast<f2*>(sm + SH::O_CK + ((j * 2 + q) * PB + pl) * NP + s * NT);
+#pragma unroll
+                for (int i = 0; i < NT / 2; i++) ck[i] = h[q][i];
+            }
+            if (j + 1 < pieces) {
+#pragma unroll
+                for (int k = 0; k < K; k++) {
+                    const int u = j * K + k;
+                    const float4 d = dd[u * PB];
+                    const float dv[2] = {d.x, d.y}, xv[2] = {d.z, d.w};
+                    f2 B[NT / 2];
+                    load_pairs(B, sm + SH::O_BC + u * 2 * NP + s * NT);
+#pragma unroll
+                    for (int q = 0; q < 2; q++)
+#pragma unroll
+                        for (int i = 0; i < NT / 2; i++)
+                            h[q][i] = fma2(ex2_2(mul2(pack2(dv[q], dv[q]), A2[q][i])), h[q][i],
+                                           mul2(pack2(xv[q], xv[q]), B[i]));
+                }
+            }
+        }
+        for (int j = pieces - 1; j >= 0; j--) {
+            f2 hp[K][2][NT / 2], dec[K][2][NT / 2];     // state before token k, decay of token k
+#pragma unroll
+            for (int q = 0; q < 2; q++)
+                load_pairs(h[q], sm + SH::O_CK + ((j * 2 + q) * PB + pl) * NP + s * NT);
 #pragma unroll
             for (int k = 0; k < K; k++) {
+                const int u = j * K + k;     // zero past the end: the state stays
+                const float4 d = dd[u * PB];
+                const float dv[2] = {d.x, d.y}, xv[2] = {d.z, d.w};
+                f2 B[NT / 2];
+                load_pairs(B, sm + SH::O_BC + u * 2 * NP + s * NT);
+#pragma unroll
+                for (int q = 0; q < 2; q++)
+#pragma unroll
+                    for (int i = 0; i < NT / 2; i++) {
+                        hp[k][q][i] = h[q][i];
+                        dec[k][q][i] = ex2_2(mul2(pack2(dv[q], dv[q]), A2[q][i]));
+                        h[q][i] = fma2(dec[k][q][i], h[q][i], mul2(pack2(xv[q], xv[q]), B[i]));
+                    }
+            }
+            // sums over the states of both channels: C h, lam B, A2 lam a h_before
+            float yv[2][K], lb[2][K], la[2][K];
+#pragma unroll
+            for (int k = K - 1; k >= 0; k--) {
                 const int u = j * K + k;
-                const float delta = sm[SH::O_DELTA + u * CB + cl], dx = sm[SH::O_DX + u * CB + cl];
-                float B[NT];
-                load_states(B, sm + SH::O_BC + u * 2 * NP + s * NT);
+                const float4 d = dd[u * PB];
+                const float2 e2 = ee[u * PB];
+                const float dv[2] = {d.x, d.y}, xv[2] = {d.z, d.w}, ev[2] = {e2.x, e2.y};
+                f2 B[NT / 2], C[NT / 2], ob[NT / 2], oc[NT / 2];
+                load_pairs(B, sm + SH::O_BC + u * 2 * NP + s * NT);
+                load_pairs(C, sm + SH::O_BC + (u * 2 + 1) * NP + s * NT);
 #pragma unroll
-                for (int i = 0; i < NT; i++) h[i] = fmaf(ex2(delta * A2[i]), h[i], dx * B[i]);
-            }
-        }
-    }
-    for (int j = pieces - 1; j >= 0; j--) {
-        float hp[K][NT], dec[K][NT];     // state before token k, decay of token k
-        load_states(h, sm + SH::O_CK + (j * CB + cl) * NP + s * NT);
+                for (int q = 0; q < 2; q++) {
+                    const f2 delta = pack2(dv[q], dv[q]), dx = pack2(xv[q], xv[q]), e = pack2(ev[q], ev[q]);
+                    f2 y = 0, b = 0, l = 0;
 #pragma unroll
-        for (int k = 0; k < K; k++) {
-            const int u = j * K + k;     // zero past the end: the state stays
-            const float delta = sm[SH::O_DELTA + u * CB + cl], dx = sm[SH::O_DX + u * CB + cl];
-            float B[NT];
-            load_states(B, sm + SH::O_BC + u * 2 * NP + s * NT);
+                    for (int i = 0; i < NT / 2; i++) {
+                        const f2 now = k == K - 1 ? h[q][i] : hp[k == K - 1 ? k : k + 1][q][i];
+                        lam[q][i] = fma2(C[i], e, lam[q][i]);
+                        ob[i] = q == 0 ? mul2(lam[q][i], dx) : fma2(lam[q][i], dx, ob[i]);
+                        oc[i] = q == 0 ? mul2(now, e) : fma2(now, e, oc[i]);
+                        y = i == 0 ? mul2(C[i], now) : fma2(C[i], now, y);
+                        b = i == 0 ? mul2(lam[q][i], B[i]) : fma2(lam[q][i], B[i], b);
+                        lam[q][i] = mul2(lam[q][i], dec[k][q][i]);
+                        const f2 lh = mul2(lam[q][i], hp[k][q][i]);
+                        l = i == 0 ? mul2(lh, A2[q][i]) : fma2(lh, A2[q][i], l);
+                        dA[q][i] = fma2(lh, delta, dA[q][i]);
+                    }
+                    yv[q][k] = sum2(y);
+                    lb[q][k] = sum2(b);
+                    la[q][k] = sum2(l);
+                }
+                // over the warp's channels
+                float over[2 * NT];
 #pragma unroll
-            for (int i = 0; i < NT; i++) {
-                hp[k][i] = h[i];
-                dec[k][i] = ex2(delta * A2[i]);
-                h[i] = fmaf(dec[k][i], h[i], dx * B[i]);
-            }
-        }
-        float yv[K], lb[K], la[K];       // sums over the states: C h, lam B, A2 lam a h_before
+                for (int i = 0; i < NT / 2; i++) {
+                    unpack2(ob[i], over[2 * i], over[2 * i + 1]);
+                    unpack2(oc[i], over[NT + 2 * i], over[NT + 2 * i + 1]);
+                }
+                const int off = lane_sum<2 * NT, CW, 1>(over, lane);
+                constexpr int HOLD = 2 * NT > CW ? 2 * NT / CW : 1, SPARE = CW > 2 * NT ? CW / (2 * NT) : 1;
+                if (lane % SPARE == 0) {
+                    float* red = sm + SH::O_RED + (wid * K + k) * 2 * NP;
 #pragma unroll
-        for (int k = K - 1; k >= 0; k--) {
-            const int u = j * K + k;
-            const float delta = sm[SH::O_DELTA + u * CB + cl], dx = sm[SH::O_DX + u * CB + cl],
-                        e = sm[SH::O_E + u * CB + cl];
-            float B[NT], C[NT], over[2 * NT];
-            load_states(B, sm + SH::O_BC + u * 2 * NP + s * NT);
-            load_states(C, sm + SH::O_BC + (u * 2 + 1) * NP + s * NT);
-            yv[k] = lb[k] = la[k] = 0.f;
-#pragma unroll
-            for (int i = 0; i < NT; i++) {
-                const float now = k == K - 1 ? h[i] : hp[k == K - 1 ? k : k + 1][i];
-                lam[i] = fmaf(C[i], e, lam[i]);
-                over[i] = lam[i] * dx;
-                over[NT + i] = now * e;
-                yv[k] = fmaf(C[i], now, yv[k]);
-                lb[k] = fmaf(lam[i], B[i], lb[k]);
-                lam[i] *= dec[k][i];
-                const float q = lam[i] * hp[k][i];
-                la[k] = fmaf(q, A2[i], la[k]);
-                dA[i] = fmaf(q, delta, dA[i]);
-            }
-            // over the warp's channels
-            const int off = lane_sum<2 * NT, CW, 1>(over, lane);
-            constexpr int HOLD = 2 * NT > CW ? 2 * NT / CW : 1, SPARE = CW > 2 * NT ? CW / (2 * NT) : 1;
-            if (lane % SPARE == 0) {
-                float* red = sm + SH::O_RED + (wid * K + k) * 2 * NP;
-#pragma unroll
-                for (int i = 0; i < HOLD; i++) {
-                    const int v = off + i;
-                    red[(v / NT) * NP + s * NT + v % NT] = over[i];
+                    for (int i = 0; i < HOLD; i++) {
+                        const int v = off + i;
+                        red[(v / NT) * NP + s * NT + v % NT] = over[i];
+                    }
                 }
             }
-        }
-        // over the channel's lanes: each ends with the sums of K / S tokens
-        const int off = lane_sum<K, S, CW>(yv, lane);
-        lane_sum<K, S, CW>(lb, lane);
-        lane_sum<K, S, CW>(la, lane);
-        constexpr int HOLD = K > S ? K / S : 1, SPARE = S > K ? S / K : 1;
-        if (live && s % SPARE == 0) {
+            // over the pair's lanes: each ends with the sums of K / S tokens, or S / K lanes with
+            // those of the same one
+            const int off = lane_sum<K, S, CW>(yv[0], lane);
+            lane_sum<K, S, CW>(yv[1], lane);
 #pragma unroll
-            for (int i = 0; i < HOLD; i++) {
-                const int u = j * K + off + i, t = p.t0 + u;
-                if (t >= end) continue;
-                const float delta = sm[SH::O_DELTA + u * CB + cl], e = sm[SH::O_E + u * CB + cl];
-                const float x = to_f(X.at(p.b, t)[c]);
-                if (a.z.p) {
-                    const float z = to_f(Z.at(p.b, t)[c]), dy = to_f(DY.at(p.b, t)[c]);
-                    const float sg = sigmoid_f<IO>(z);
-                    const float y = fmaf(skip, x, yv[i]);
-                    DZ.at(p.b, t)[c] = from_f<IO>(dy * y * sg * (1.f + z * (1.f - sg)));
-                }
-                float ddt = fmaf(x, lb[i], la[i] * kLn2);
-                if (a.softplus) ddt *= sigmoid_f<IO>(to_f(DT.at(p.b, t)[c]) + bias);
-                DX.at(p.b, t)[c] = from_f<IO>(fmaf(delta, lb[i], skip * e));
-                DDT.at(p.b, t)[c] = from_f<IO>(ddt);
-                dD = fmaf(e, x, dD);
-                dbias += ddt;
+            for (int q = 0; q < 2; q++) {
+                lane_sum<K, S, CW>(lb[q], lane);
+                lane_sum<K, S, CW>(la[q], lane);
             }
-        }
-        // over the block's warps, to the workspace
-        __syncthreads();
-        for (int i = threadIdx.x; i < K * 2 * NP; i += SH::THREADS) {
-            float v = 0.f;
+            constexpr int TOKENS = K > S ? K / S : 1, SAME = S > K ? S / K : 1;
+            if (mine && s % SAME == 0) {
 #pragma unroll
-            for (int w = 0; w < WARPS; w++) v += sm[SH::O_RED + w * K * 2 * NP + i];
-            const int t = p.t0 + j * K + i / (2 * NP);
-            if (t < end)
-                a.pBC[(((long long)p.b * a.T + t) * tiles + tile) * 2 * NP + i % (2 * NP)] = v;
+                for (int i = 0; i < TOKENS; i++) {
+                    const int u = j * K + off + i, t = t0 + u;
+                    if (t >= end) continue;
+                    const float4 d = dd[u * PB];
+                    const float2 e = ee[u * PB];
+                    const float2 x = load_two<IO, WIDE>(X.at(p.b, t) + c, mine == 2);
+                    float o[2];
+                    if (a.z.p) {
+                        const float2 z = load_two<IO, WIDE>(Z.at(p.b, t) + c, mine == 2);
+                        const float2 dy = load_two<IO, WIDE>(DY.at(p.b, t) + c, mine == 2);
+                        const float s0 = sigmoid_f<IO>(z.x), s1 = sigmoid_f<IO>(z.y);
+                        o[0] = dy.x * fmaf(skip[0], x.x, yv[0][i]) * fmaf(z.x * s0, 1.f - s0, s0);
+                        o[1] = dy.y * fmaf(skip[1], x.y, yv[1][i]) * fmaf(z.y * s1, 1.f - s1, s1);
+                        Vec<IO, 2>::template store<WIDE>(o, DZ.at(p.b, t) + c, mine);
+                    }
+                    o[0] = fmaf(d.x, lb[0][i], skip[0] * e.x);
+                    o[1] = fmaf(d.y, lb[1][i], skip[1] * e.y);
+                    Vec<IO, 2>::template store<WIDE>(o, DX.at(p.b, t) + c, mine);
+                    o[0] = fmaf(x.x, lb[0][i], la[0][i] * kLn2);
+                    o[1] = fmaf(x.y, lb[1][i], la[1][i] * kLn2);
+                    if (a.softplus) {
+                        const float2 dt = load_two<IO, WIDE>(DT.at(p.b, t) + c, mine == 2);
+                        o[0] *= sigmoid_f<IO>(dt.x + bias[0]);
+                        o[1] *= sigmoid_f<IO>(dt.y + bias[1]);
+                    }
+                    Vec<IO, 2>::template store<WIDE>(o, DDT.at(p.b, t) + c, mine);
+                    dD[0] = fmaf(e.x, x.x, dD[0]);
+                    dD[1] = fmaf(e.y, x.y, dD[1]);
+                    dbias[0] += o[0];
+                    dbias[1] += o[1];
+                }
+            }
+            // over the block's warps, to the workspace
+            __syncthreads();
+            for (int i = threadIdx.x; i < K * 2 * NP; i += SH::THREADS) {
+                float v = 0.f;
+#pragma unroll
+                for (int w = 0; w < WARPS; w++) v += sm[SH::O_RED + w * K * 2 * NP + i];
+                const int t = t0 + j * K + i / (2 * NP);
+                if (t < end)
+                    a.pBC[(((long long)p.b * a.T + t) * blks + blk) * 2 * NP + i % (2 * NP)] = v;
+            }
+            __syncthreads();
         }
-        __syncthreads();
     }
     // rows past the sequence's length
     for (int t = max(p.t0, p.len); t < p.t1; t++)
@@ -326,20 +446,17 @@ __global__ void __launch_bounds__(SH::THREADS) sel_bwd_kernel(const SelArgs a) {
             if (a.z.p) DZ.at(p.b, t)[p.c0 + k] = from_f<IO>(0.f);
         }
 #pragma unroll
-    for (int o = CW; o < 32; o *= 2) {
-        dD += __shfl_xor_sync(0xffffffffu, dD, o);
-        dbias += __shfl_xor_sync(0xffffffffu, dbias, o);
-    }
-    if (live) {
+    for (int q = 0; q < 2; q++) {
 #pragma unroll
-        for (int i = 0; i < NT; i++) {
-            const int n = s * NT + i;
-            if (n < a.N) a.pA[row + n] = dA[i];
+        for (int o = CW; o < 32; o *= 2) {
+            dD[q] += __shfl_xor_sync(0xffffffffu, dD[q], o);
+            dbias[q] += __shfl_xor_sync(0xffffffffu, dbias[q], o);
         }
-        if (s == 0) {
-            float* q = a.pD + ((long long)p.b * a.nseg + p.seg) * 2 * a.D + c;
-            q[0] = dD;
-            q[a.D] = dbias;
+        store_pairs<NT>(dA[q], a.pA + row + q * a.N, q < mine, s * NT, a.N);
+        if (q < mine && s == 0) {
+            float* o = a.pD + ((long long)p.b * a.nseg + p.seg) * 2 * a.D + c + q;
+            o[0] = dD[q];
+            o[a.D] = dbias[q];
         }
     }
 }
@@ -391,20 +508,21 @@ __global__ void __launch_bounds__(256) sel_bwd_sum_kernel(const float* part, int
     }
 }
 
-template <typename IO, typename SH>
-cudaError_t bwd_t(const SelArgs& a, cudaStream_t s) {
+template <typename IO, typename SH, bool WIDE>
+cudaError_t bwd_w(const SelArgs& a, cudaStream_t s) {
     const int tiles = sel_tiles(a.D, a.G, SH::CB);
     const unsigned grid = (unsigned)((long long)tiles * a.nseg * a.batch);
-    cudaError_t e = cudaFuncSetAttribute(sel_bwd_local_kernel<IO, SH>,
+    cudaError_t e = cudaFuncSetAttribute(sel_bwd_local_kernel<IO, SH, WIDE>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, SH::LOCAL_BYTES);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(sel_bwd_kernel<IO, SH>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 SH::BYTES);
+        e = cudaFuncSetAttribute(sel_bwd_kernel<IO, SH, WIDE>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, SH::BYTES);
     if (e != cudaSuccess) return e;
-    sel_bwd_local_kernel<IO, SH><<<grid, SH::THREADS, SH::LOCAL_BYTES, s>>>(a);
+    sel_bwd_local_kernel<IO, SH, WIDE><<<grid, SH::THREADS, SH::LOCAL_BYTES, s>>>(a);
     const long long states = (long long)a.D * a.N;
-    sel_bwd_chain_kernel<<<(unsigned)((states * a.batch + 127) / 128), 128, 0, s>>>(a);
-    sel_bwd_kernel<IO, SH><<<grid, SH::THREADS, SH::BYTES, s>>>(a);
+    const int blocks = (int)((states * a.batch + 127) / 128);
+    sel_bwd_chain_kernel<<<2 * blocks, 128, 0, s>>>(a, blocks);
+    sel_bwd_kernel<IO, SH, WIDE><<<grid, SH::THREADS, SH::BYTES, s>>>(a);
     const long long bc = (long long)a.batch * a.T * a.G * 2 * a.N;
     sel_bwd_bc_kernel<IO><<<(unsigned)((bc + 255) / 256), 256, 0, s>>>(a, SH::NP, tiles);
     const int rows = a.batch * a.nseg;
@@ -416,50 +534,64 @@ cudaError_t bwd_t(const SelArgs& a, cudaStream_t s) {
     return cudaGetLastError();
 }
 
-template <typename IO, typename F>
+template <typename IO, typename SH>
+cudaError_t bwd_t(const SelArgs& a, cudaStream_t s) {
+    return a.wide ? bwd_w<IO, SH, true>(a, s) : bwd_w<IO, SH, false>(a, s);
+}
+
+// The lane shape by the number of states.
+template <typename F>
 cudaError_t by_n(int N, F f) {
-    if (N <= 4) return f(BwdShape<4, 1, 2, 64, 8>{});
-    if (N <= 8) return f(BwdShape<4, 2, 4, 64, 8>{});
-    if (N <= 16) return f(BwdShape<4, 4, 8, 64, 8>{});
-    if (N <= 32) return f(BwdShape<4, 8, 8, 64, 8>{});
-    if (N <= 64) return f(BwdShape<8, 8, 8, 32, 4>{});
-    if (N <= 128) return f(BwdShape<8, 16, 8, 32, 4>{});
-    return f(BwdShape<8, 32, 8, 32, 4>{});
+    if (N <= 4) return f(BwdShape<4, 1, 2, 32, 4>{});
+    if (N <= 8) return f(BwdShape<4, 2, 2, 32, 4>{});
+    if (N <= 16) return f(BwdShape<4, 4, 4, 32, 4>{});
+    if (N <= 32) return f(BwdShape<4, 8, 4, 32, 4>{});
+    if (N <= 64) return f(BwdShape<4, 16, 4, 32, 4>{});
+    if (N <= 128) return f(BwdShape<8, 16, 4, 16, 2>{});
+    return f(BwdShape<8, 32, 4, 16, 2>{});
 }
 
 }  // namespace
 
-size_t sel_bwd_plan(SelArgs* a, int io_dtype, char* ws) {
+size_t sel_bwd_plan(SelArgs* a, char* ws) {
     int NP = 0, CB = 0;
-    by_n<float>(a->N, [&](auto sh) {
+    by_n(a->N, [&](auto sh) {
         using SH = decltype(sh);
-        a->seg = SH::L;
+        a->tile = SH::L;
         NP = SH::NP;
         CB = SH::CB;
         return cudaSuccess;
     });
-    a->nseg = (a->T + a->seg - 1) / a->seg;
+    const size_t blks = sel_tiles(a->D, a->G, CB);
+    a->ntile = (a->T + a->tile - 1) / a->tile;
+    // Tiles of a segment: four where the segments still give every SM its blocks several times
+    // over (fewer segments are chained, and fewer shares of dA summed), else fewer.
+    int m = 4;
+    while (m > 1 && (long long)blks * a->batch * ((a->ntile + m - 1) / m) < 148 * 12) m /= 2;
+    a->seg = m * a->tile;
+    a->nseg = (a->ntile + m - 1) / m;
     const size_t runs = (size_t)a->batch * a->nseg, states = (size_t)a->D * a->N;
-    const size_t tiles = sel_tiles(a->D, a->G, CB);
+    const size_t all = (size_t)a->batch * a->ntile;
     size_t at = 0;
     auto take = [&](size_t floats) {
         float* p = reinterpret_cast<float*>(ws + at);
         at += (floats * sizeof(float) + 255) / 256 * 256;
         return p;
     };
+    a->hloc = take(all * states);
+    a->dsum = take(all * a->D);
     a->hseg = take(runs * states);
     a->gseg = take(runs * states);
     a->pA = take(runs * states);
-    a->dsum = take(runs * a->D);
     a->pD = take(runs * 2 * a->D);
-    a->pBC = take((size_t)a->batch * a->T * tiles * 2 * NP);
+    a->pBC = take((size_t)a->batch * a->T * blks * 2 * NP);
     return at;
 }
 
 cudaError_t launch_sel_bwd(const SelArgs& a, int io_dtype, cudaStream_t s) {
     if (io_dtype == M3_BF16)
-        return by_n<__nv_bfloat16>(a.N, [&](auto sh) { return bwd_t<__nv_bfloat16, decltype(sh)>(a, s); });
-    return by_n<float>(a.N, [&](auto sh) { return bwd_t<float, decltype(sh)>(a, s); });
+        return by_n(a.N, [&](auto sh) { return bwd_t<__nv_bfloat16, decltype(sh)>(a, s); });
+    return by_n(a.N, [&](auto sh) { return bwd_t<float, decltype(sh)>(a, s); });
 }
 
 }  // namespace m3

@@ -40,15 +40,6 @@ struct FwdSmem {
     alignas(16) float4 dd[L][CB / 2];     // of two channels: delta, delta, delta x, delta x
 };
 
-template <typename IO>
-__device__ __forceinline__ float2 pair_of(const IO* p) {
-    if constexpr (sizeof(IO) == 2) {
-        return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p));
-    } else {
-        return *reinterpret_cast<const float2*>(p);
-    }
-}
-
 template <typename IO, typename SH, bool WIDE, bool LOCAL>
 __global__ void __launch_bounds__(SH::THREADS) sel_scan_kernel(const SelArgs a) {
     constexpr int L = SH::L, NT = SH::NT, S = SH::S, CW = SH::CW, CB = SH::CB * 2, NP = SH::NP;

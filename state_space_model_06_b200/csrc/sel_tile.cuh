@@ -99,6 +99,16 @@ __device__ __forceinline__ void stage_rows(IO* sm, const View& v, int b, long lo
     }
 }
 
+// Two neighbouring values as floats.
+template <typename IO>
+__device__ __forceinline__ float2 pair_of(const IO* p) {
+    if constexpr (sizeof(IO) == 2) {
+        return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p));
+    } else {
+        return *reinterpret_cast<const float2*>(p);
+    }
+}
+
 // B and C of tokens t0 .. t0 + L - 1 as floats in sm[L][2][NP]; tokens at or past `end` and
 // states past N read zero.
 template <typename IO, int NP, int L, int THREADS>
