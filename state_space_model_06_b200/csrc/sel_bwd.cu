@@ -37,8 +37,8 @@ struct BwdShape {
     static constexpr int CB = 2 * PB;            // channels of a block
     static constexpr int NP = NT * S;            // states, padded
     static constexpr int THREADS = 32 * WARPS;
-    static constexpr int MIN_BLOCKS = NT * K <= 16 ? 512 / THREADS : 1;   // 128 registers a thread
-    static constexpr int LOCAL_BLOCKS = NT == 4 ? 768 / THREADS : 1;      // 80 registers
+    static constexpr int MIN_BLOCKS = NT * K <= 16 ? 384 / THREADS : 1;   // 168 registers a thread
+    static constexpr int LOCAL_BLOCKS = NT == 4 ? 640 / THREADS : 1;      // 102 registers
     // shared memory, in floats
     static constexpr int O_BC = 0;                              // [L][2][NP]
     static constexpr int O_DD = O_BC + L * 2 * NP;              // [L][PB] float4: delta, delta x of two channels
@@ -46,51 +46,89 @@ struct BwdShape {
     static constexpr int O_CK = O_E + L * PB * 2;               // [L / K][CB][NP]
     static constexpr int O_RED = O_CK + L / K * CB * NP;        // [WARPS][K][2 NP]
     static constexpr int LOCAL_BYTES = 4 * O_CK;
-    static constexpr int BYTES = 4 * (O_RED + WARPS * K * 2 * NP);
+    static constexpr int RED = WARPS * K * 2 * NP;              // twice: of a piece and the one before
+    static constexpr int BYTES = 4 * (O_RED + 2 * RED);
     static_assert(BYTES <= 227 * 1024 && THREADS % PB == 0, "");
 };
 
-// Two neighbouring values of a row (`two` false: the second is not there).
+// Two neighbouring values of a row, as they are (`two` false: the second is not there).
+template <typename IO>
+struct Two;
+template <>
+struct Two<float> {
+    float2 v;
+    __device__ __forceinline__ float2 f() const { return v; }
+};
+template <>
+struct Two<__nv_bfloat16> {
+    uint32_t v;       // one register, loaded as one word
+    __device__ __forceinline__ float2 f() const {
+        return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+    }
+};
 template <typename IO, bool WIDE>
-__device__ __forceinline__ float2 load_two(const IO* p, bool two) {
-    if constexpr (WIDE) return pair_of(p);
-    return make_float2(to_f(p[0]), two ? to_f(p[1]) : 0.f);
+__device__ __forceinline__ Two<IO> load_two(const IO* p, bool two) {
+    Two<IO> r;
+    if constexpr (WIDE) {
+        r.v = *reinterpret_cast<const decltype(r.v)*>(p);
+    } else if constexpr (sizeof(IO) == 4) {
+        r.v = make_float2(p[0], two ? p[1] : 0.f);
+    } else {
+        const unsigned short* q = reinterpret_cast<const unsigned short*>(p);
+        r.v = q[0] | (two ? (uint32_t)q[1] << 16 : 0u);
+    }
+    return r;
 }
 
 // delta, delta x and e = dy SiLU(z) of a tile's tokens (zero past the end), and B and C
 template <typename IO, typename SH, bool WIDE>
 __device__ __forceinline__ void bwd_stage(const SelArgs& a, const SelPlace& p, int t0, int end,
                                           float* sm) {
-    constexpr int PB = SH::PB;
-    const Rows<const IO> X{static_cast<const IO*>(a.x.p), a.x.bs, a.x.ts};
-    const Rows<const IO> DT{static_cast<const IO*>(a.dt.p), a.dt.bs, a.dt.ts};
-    const Rows<const IO> Z{static_cast<const IO*>(a.z.p), a.z.bs, a.z.ts};
-    const Rows<const IO> DY{static_cast<const IO*>(a.dy.p), a.dy.bs, a.dy.ts};
+    constexpr int PB = SH::PB, STEP = SH::THREADS / PB;
+    constexpr int U = SH::L / STEP < 4 ? SH::L / STEP : 4;      // tokens requested together
+    static_assert(U > 0 && SH::L % (STEP * U) == 0, "");
     sel_stage_bc<IO, SH::NP, SH::L, SH::THREADS>(a, p, t0, end, sm + SH::O_BC);
     const int k = threadIdx.x % PB, c = p.c0 + 2 * k;
     const bool one = 2 * k < p.nc, two = 2 * k + 1 < p.nc;
     const float2 bias = make_float2(one && a.dt_bias ? a.dt_bias[c] : 0.f,
                                     two && a.dt_bias ? a.dt_bias[c + 1] : 0.f);
-#pragma unroll 2
-    for (int u = threadIdx.x / PB; u < SH::L; u += SH::THREADS / PB) {
-        const int t = t0 + u;
-        float2 delta = make_float2(0.f, 0.f), dx = delta, e = delta;
-        if (t < end && one) {
-            const float2 dt = load_two<IO, WIDE>(DT.at(p.b, t) + c, two);
-            const float2 x = load_two<IO, WIDE>(X.at(p.b, t) + c, two);
-            e = load_two<IO, WIDE>(DY.at(p.b, t) + c, two);
-            if (a.z.p) {
-                const float2 z = load_two<IO, WIDE>(Z.at(p.b, t) + c, two);
-                e.x *= z.x * sigmoid_f<IO>(z.x);
-                e.y *= z.y * sigmoid_f<IO>(z.y);
+    const IO* x = static_cast<const IO*>(a.x.p) + p.b * a.x.bs + c;
+    const IO* dt = static_cast<const IO*>(a.dt.p) + p.b * a.dt.bs + c;
+    const IO* z = static_cast<const IO*>(a.z.p) + p.b * a.z.bs + c;
+    const IO* dy = static_cast<const IO*>(a.dy.p) + p.b * a.dy.bs + c;
+#pragma unroll 1
+    for (int u0 = threadIdx.x / PB; u0 < SH::L; u0 += STEP * U) {
+        Two<IO> rx[U], rt[U], rz[U], ry[U];
+#pragma unroll
+        for (int i = 0; i < U; i++) {
+            const long long t = t0 + u0 + i * STEP;
+            if (t < end && one) {
+                rx[i] = load_two<IO, WIDE>(x + t * a.x.ts, two);
+                rt[i] = load_two<IO, WIDE>(dt + t * a.dt.ts, two);
+                ry[i] = load_two<IO, WIDE>(dy + t * a.dy.ts, two);
+                if (a.z.p) rz[i] = load_two<IO, WIDE>(z + t * a.z.ts, two);
             }
-            delta.x = sel_delta(dt.x, bias.x, a.softplus);
-            delta.y = two ? sel_delta(dt.y, bias.y, a.softplus) : 0.f;
-            dx.x = delta.x * x.x;
-            dx.y = delta.y * x.y;
         }
-        reinterpret_cast<float4*>(sm + SH::O_DD)[u * PB + k] = make_float4(delta.x, delta.y, dx.x, dx.y);
-        reinterpret_cast<float2*>(sm + SH::O_E)[u * PB + k] = e;
+#pragma unroll
+        for (int i = 0; i < U; i++) {
+            const int u = u0 + i * STEP;
+            float2 delta = make_float2(0.f, 0.f), dx = delta, e = delta;
+            if (t0 + u < end && one) {
+                const float2 xv = rx[i].f(), tv = rt[i].f();
+                e = ry[i].f();
+                if (a.z.p) {
+                    const float2 zv = rz[i].f();
+                    e.x *= zv.x * sigmoid_f<IO>(zv.x);
+                    e.y *= zv.y * sigmoid_f<IO>(zv.y);
+                }
+                delta.x = sel_delta(tv.x, bias.x, a.softplus);
+                delta.y = two ? sel_delta(tv.y, bias.y, a.softplus) : 0.f;
+                dx.x = delta.x * xv.x;
+                dx.y = delta.y * xv.y;
+            }
+            reinterpret_cast<float4*>(sm + SH::O_DD)[u * PB + k] = make_float4(delta.x, delta.y, dx.x, dx.y);
+            reinterpret_cast<float2*>(sm + SH::O_E)[u * PB + k] = e;
+        }
     }
 }
 
@@ -311,6 +349,22 @@ __global__ void __launch_bounds__(SH::THREADS, SH::MIN_BLOCKS) sel_bwd_kernel(co
             }
         }
         for (int j = pieces - 1; j >= 0; j--) {
+            // the tokens whose sums this lane ends with, and their values, on their way early
+            constexpr int TOKENS = K > S ? K / S : 1, SAME = S > K ? S / K : 1;
+            const int own = s / SAME * TOKENS;
+            Two<IO> rx[TOKENS], rt[TOKENS], rz[TOKENS], ry[TOKENS];
+#pragma unroll
+            for (int i = 0; i < TOKENS; i++) {
+                const int t = t0 + j * K + own + i;
+                if (mine && t < end) {
+                    rx[i] = load_two<IO, WIDE>(X.at(p.b, t) + c, mine == 2);
+                    if (a.softplus) rt[i] = load_two<IO, WIDE>(DT.at(p.b, t) + c, mine == 2);
+                    if (a.z.p) {
+                        rz[i] = load_two<IO, WIDE>(Z.at(p.b, t) + c, mine == 2);
+                        ry[i] = load_two<IO, WIDE>(DY.at(p.b, t) + c, mine == 2);
+                    }
+                }
+            }
             f2 hp[K][2][NT / 2], dec[K][2][NT / 2];     // state before token k, decay of token k
 #pragma unroll
             for (int q = 0; q < 2; q++)
@@ -373,7 +427,7 @@ __global__ void __launch_bounds__(SH::THREADS, SH::MIN_BLOCKS) sel_bwd_kernel(co
                 const int off = lane_sum<2 * NT, CW, 1>(over, lane);
                 constexpr int HOLD = 2 * NT > CW ? 2 * NT / CW : 1, SPARE = CW > 2 * NT ? CW / (2 * NT) : 1;
                 if (lane % SPARE == 0) {
-                    float* red = sm + SH::O_RED + (wid * K + k) * 2 * NP;
+                    float* red = sm + SH::O_RED + (j & 1) * SH::RED + (wid * K + k) * 2 * NP;
 #pragma unroll
                     for (int i = 0; i < HOLD; i++) {
                         const int v = off + i;
@@ -383,26 +437,23 @@ __global__ void __launch_bounds__(SH::THREADS, SH::MIN_BLOCKS) sel_bwd_kernel(co
             }
             // over the pair's lanes: each ends with the sums of K / S tokens, or S / K lanes with
             // those of the same one
-            const int off = lane_sum<K, S, CW>(yv[0], lane);
-            lane_sum<K, S, CW>(yv[1], lane);
 #pragma unroll
             for (int q = 0; q < 2; q++) {
+                lane_sum<K, S, CW>(yv[q], lane);
                 lane_sum<K, S, CW>(lb[q], lane);
                 lane_sum<K, S, CW>(la[q], lane);
             }
-            constexpr int TOKENS = K > S ? K / S : 1, SAME = S > K ? S / K : 1;
             if (mine && s % SAME == 0) {
 #pragma unroll
                 for (int i = 0; i < TOKENS; i++) {
-                    const int u = j * K + off + i, t = t0 + u;
+                    const int u = j * K + own + i, t = t0 + u;
                     if (t >= end) continue;
                     const float4 d = dd[u * PB];
                     const float2 e = ee[u * PB];
-                    const float2 x = load_two<IO, WIDE>(X.at(p.b, t) + c, mine == 2);
+                    const float2 x = rx[i].f();
                     float o[2];
                     if (a.z.p) {
-                        const float2 z = load_two<IO, WIDE>(Z.at(p.b, t) + c, mine == 2);
-                        const float2 dy = load_two<IO, WIDE>(DY.at(p.b, t) + c, mine == 2);
+                        const float2 z = rz[i].f(), dy = ry[i].f();
                         const float s0 = sigmoid_f<IO>(z.x), s1 = sigmoid_f<IO>(z.y);
                         o[0] = dy.x * fmaf(skip[0], x.x, yv[0][i]) * fmaf(z.x * s0, 1.f - s0, s0);
                         o[1] = dy.y * fmaf(skip[1], x.y, yv[1][i]) * fmaf(z.y * s1, 1.f - s1, s1);
@@ -414,7 +465,7 @@ __global__ void __launch_bounds__(SH::THREADS, SH::MIN_BLOCKS) sel_bwd_kernel(co
                     o[0] = fmaf(x.x, lb[0][i], la[0][i] * kLn2);
                     o[1] = fmaf(x.y, lb[1][i], la[1][i] * kLn2);
                     if (a.softplus) {
-                        const float2 dt = load_two<IO, WIDE>(DT.at(p.b, t) + c, mine == 2);
+                        const float2 dt = rt[i].f();
                         o[0] *= sigmoid_f<IO>(dt.x + bias[0]);
                         o[1] *= sigmoid_f<IO>(dt.y + bias[1]);
                     }
@@ -430,12 +481,11 @@ __global__ void __launch_bounds__(SH::THREADS, SH::MIN_BLOCKS) sel_bwd_kernel(co
             for (int i = threadIdx.x; i < K * 2 * NP; i += SH::THREADS) {
                 float v = 0.f;
 #pragma unroll
-                for (int w = 0; w < WARPS; w++) v += sm[SH::O_RED + w * K * 2 * NP + i];
+                for (int w = 0; w < WARPS; w++) v += sm[SH::O_RED + (j & 1) * SH::RED + w * K * 2 * NP + i];
                 const int t = t0 + j * K + i / (2 * NP);
                 if (t < end)
                     a.pBC[(((long long)p.b * a.T + t) * blks + blk) * 2 * NP + i % (2 * NP)] = v;
             }
-            __syncthreads();
         }
     }
     // rows past the sequence's length
@@ -548,7 +598,7 @@ cudaError_t by_n(int N, F f) {
     if (N <= 32) return f(BwdShape<4, 8, 4, 32, 4>{});
     if (N <= 64) return f(BwdShape<4, 16, 4, 32, 4>{});
     if (N <= 128) return f(BwdShape<8, 16, 4, 16, 2>{});
-    return f(BwdShape<8, 32, 4, 16, 2>{});
+    return f(BwdShape<8, 32, 2, 32, 2>{});
 }
 
 }  // namespace
