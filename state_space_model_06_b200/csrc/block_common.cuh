@@ -58,6 +58,13 @@ __device__ __forceinline__ float softplus_f(float v) {
     return fmaxf(v, 0.f) + fmaf(r * q, t, t);
 }
 
+// A kernel may use `bytes` of dynamic shared memory (above the 48 KiB that every kernel may).
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes) {
+    if (bytes <= 48 * 1024) return cudaSuccess;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
 // ------------------------------------------------------------------ packed pairs
 // Two fp32 values in a 64-bit register pair: one FFMA2 does the work of two FFMAs in one issue
 // slot, and these kernels are short of issue slots.

@@ -400,6 +400,7 @@ __global__ void __launch_bounds__(256) conv_bwd_sum_kernel(const float* part, in
     const int c = blockIdx.x * 32 + lane, k = blockIdx.y;
     float s = 0.f;
     if (c < C)
+#pragma unroll 4
         for (int r = wid; r < runs; r += 8) s += part[((long long)r * (W + 1) + k) * C + c];
     sm[wid][lane] = s;
     __syncthreads();

@@ -238,6 +238,7 @@ __global__ void __launch_bounds__(256) norm_bwd_sum_kernel(const float* part, in
     const int c = blockIdx.x * 32 + lane;
     float s = 0.f;
     if (c < d)
+#pragma unroll 8
         for (int r = wid; r < shares; r += 8) s += part[(long long)r * d + c];
     sm[wid][lane] = s;
     __syncthreads();

@@ -538,23 +538,31 @@ __global__ void __launch_bounds__(256) sel_bwd_bc_kernel(const SelArgs a, int NP
         static_cast<IO*>(a.dB.p)[b * a.dB.bs + t * a.dB.ts + at] = from_f<IO>(v);
 }
 
-// Column sums of rows x cols shares: a block per 32 columns, a warp every eighth row.
-__global__ void __launch_bounds__(256) sel_bwd_sum_kernel(const float* part, int rows,
-                                                          long long stride, long long cols,
-                                                          float* out) {
+// Column sums of the segments' shares: dA ([runs][D N]), then dD and ddt_bias ([runs][2][D]).  A
+// block per 32 columns, a warp every eighth run.
+__global__ void __launch_bounds__(256) sel_bwd_sum_kernel(const SelArgs a) {
     __shared__ float sm[8][33];
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    const long long c = blockIdx.x * 32ll + lane;
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, runs = a.batch * a.nseg;
+    const long long states = (long long)a.D * a.N, c = blockIdx.x * 32ll + lane;
+    const bool in_A = c < states, on = c < states + 2 * a.D;
+    const float* part = in_A ? a.pA + c : a.pD + (c - states);
+    const long long stride = in_A ? states : 2ll * a.D;
     float s = 0.f;
-    if (c < cols)
-        for (int r = wid; r < rows; r += 8) s += part[r * stride + c];
+    if (on)
+#pragma unroll 4
+        for (int r = wid; r < runs; r += 8) s += part[r * stride];
     sm[wid][lane] = s;
     __syncthreads();
-    if (wid == 0 && c < cols) {
+    if (wid == 0 && on) {
         float v = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; i++) v += sm[i][lane];
-        out[c] = v;
+        if (in_A)
+            a.dA[c] = v;
+        else if (c < states + a.D) {
+            if (a.dD) a.dD[c - states] = v;
+        } else if (a.ddt_bias)
+            a.ddt_bias[c - states - a.D] = v;
     }
 }
 
@@ -562,11 +570,8 @@ template <typename IO, typename SH, bool WIDE>
 cudaError_t bwd_w(const SelArgs& a, cudaStream_t s) {
     const int tiles = sel_tiles(a.D, a.G, SH::CB);
     const unsigned grid = (unsigned)((long long)tiles * a.nseg * a.batch);
-    cudaError_t e = cudaFuncSetAttribute(sel_bwd_local_kernel<IO, SH, WIDE>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, SH::LOCAL_BYTES);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(sel_bwd_kernel<IO, SH, WIDE>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, SH::BYTES);
+    cudaError_t e = allow_smem(sel_bwd_local_kernel<IO, SH, WIDE>, SH::LOCAL_BYTES);
+    if (e == cudaSuccess) e = allow_smem(sel_bwd_kernel<IO, SH, WIDE>, SH::BYTES);
     if (e != cudaSuccess) return e;
     sel_bwd_local_kernel<IO, SH, WIDE><<<grid, SH::THREADS, SH::LOCAL_BYTES, s>>>(a);
     const long long states = (long long)a.D * a.N;
@@ -575,12 +580,7 @@ cudaError_t bwd_w(const SelArgs& a, cudaStream_t s) {
     sel_bwd_kernel<IO, SH, WIDE><<<grid, SH::THREADS, SH::BYTES, s>>>(a);
     const long long bc = (long long)a.batch * a.T * a.G * 2 * a.N;
     sel_bwd_bc_kernel<IO><<<(unsigned)((bc + 255) / 256), 256, 0, s>>>(a, SH::NP, tiles);
-    const int rows = a.batch * a.nseg;
-    sel_bwd_sum_kernel<<<(unsigned)((states + 31) / 32), 256, 0, s>>>(a.pA, rows, states, states, a.dA);
-    if (a.dD)
-        sel_bwd_sum_kernel<<<(a.D + 31) / 32, 256, 0, s>>>(a.pD, rows, 2ll * a.D, a.D, a.dD);
-    if (a.ddt_bias)
-        sel_bwd_sum_kernel<<<(a.D + 31) / 32, 256, 0, s>>>(a.pD + a.D, rows, 2ll * a.D, a.D, a.ddt_bias);
+    sel_bwd_sum_kernel<<<(unsigned)((states + 2 * a.D + 31) / 32), 256, 0, s>>>(a);
     return cudaGetLastError();
 }
 

@@ -380,12 +380,10 @@ cudaError_t fwd_w(const SelArgs& a, cudaStream_t s) {
     constexpr int bytes = (int)sizeof(FwdSmem<IO, SH>);
     static_assert(bytes <= 227 * 1024, "");
     const unsigned grid = (unsigned)((long long)sel_tiles(a.D, a.G, 2 * SH::CB) * a.nseg * a.batch);
-    cudaError_t e = cudaFuncSetAttribute(sel_scan_kernel<IO, SH, WIDE, false>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaError_t e = allow_smem(sel_scan_kernel<IO, SH, WIDE, false>, bytes);
     if (e != cudaSuccess) return e;
     if (a.nseg > 1) {
-        e = cudaFuncSetAttribute(sel_scan_kernel<IO, SH, WIDE, true>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        e = allow_smem(sel_scan_kernel<IO, SH, WIDE, true>, bytes);
         if (e != cudaSuccess) return e;
         sel_scan_kernel<IO, SH, WIDE, true><<<grid, SH::THREADS, bytes, s>>>(a);
         const long long n = (long long)a.batch * a.D * a.N;

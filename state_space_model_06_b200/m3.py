@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass, replace
 
 import torch
@@ -143,25 +144,21 @@ def load_library(path: str = LIB_PATH):
         lib.m3_scan_bwd_ex.argtypes = [dp, i32, vp, vp, vp, vp, vp, vp, vp, vp, sp, ep, vp, vp,
                                        ctypes.POINTER(m3_grads), ctypes.POINTER(m3_extra_grads),
                                        vp, sz, u32, vp]
-        i64, rp = ctypes.c_int64, ctypes.POINTER(m3_rows)
-        cdp, sdp = ctypes.POINTER(m3_conv_dims), ctypes.POINTER(m3_sel_dims)
-        ndp, sip = ctypes.POINTER(m3_norm_dims), ctypes.POINTER(m3_sel_inputs)
-        lib.m3_conv_fwd.argtypes = [cdp, i32, rp, vp, vp, vp, vp, rp, u32, vp]
-        lib.m3_conv_step.argtypes = [cdp, rp, vp, vp, vp, rp, u32, vp]
-        lib.m3_conv_bwd_workspace_bytes.argtypes = [cdp, i32, szp]
-        lib.m3_conv_bwd.argtypes = [cdp, i32, rp, vp, vp, vp, vp, rp,
-                                    ctypes.POINTER(m3_conv_grads), vp, sz, u32, vp]
-        lib.m3_sel_workspace_bytes.argtypes = [sdp, i32, szp]
-        lib.m3_sel_fwd.argtypes = [sdp, i32, sip, vp, rp, vp, sz, u32, vp]
-        lib.m3_sel_step.argtypes = [sdp, sip, vp, rp, u32, vp]
-        lib.m3_sel_bwd_workspace_bytes.argtypes = [sdp, i32, szp]
-        lib.m3_sel_bwd.argtypes = [sdp, i32, sip, vp, rp, vp, ctypes.POINTER(m3_sel_grads), vp, sz,
-                                   u32, vp]
-        lib.m3_norm_fwd.argtypes = [ndp, vp, i64, vp, i64, vp, ctypes.c_float, vp, i64, vp, vp, i64,
-                                    vp]
-        lib.m3_norm_bwd_workspace_bytes.argtypes = [ndp, szp]
-        lib.m3_norm_bwd.argtypes = [ndp, vp, i64, vp, ctypes.c_float, vp, i64, vp, i64, vp, i64, vp,
-                                    i64, vp, vp, sz, vp]
+        # block operators: structs are passed as packed bytes (see _PACK_ROWS)
+        i64, f32 = ctypes.c_int64, ctypes.c_float
+        lib.m3_conv_fwd.argtypes = [vp, i32, vp, vp, vp, vp, vp, vp, u32, vp]
+        lib.m3_conv_step.argtypes = [vp, vp, vp, vp, vp, vp, u32, vp]
+        lib.m3_conv_bwd_workspace_bytes.argtypes = [vp, i32, szp]
+        lib.m3_conv_bwd.argtypes = [vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, u32, vp]
+        lib.m3_sel_workspace_bytes.argtypes = [vp, i32, szp]
+        lib.m3_sel_fwd.argtypes = [vp, i32, vp, vp, vp, vp, sz, u32, vp]
+        lib.m3_sel_step.argtypes = [vp, vp, vp, vp, u32, vp]
+        lib.m3_sel_bwd_workspace_bytes.argtypes = [vp, i32, szp]
+        lib.m3_sel_bwd.argtypes = [vp, i32, vp, vp, vp, vp, vp, vp, sz, u32, vp]
+        lib.m3_norm_fwd.argtypes = [vp, vp, i64, vp, i64, vp, f32, vp, i64, vp, vp, i64, vp]
+        lib.m3_norm_bwd_workspace_bytes.argtypes = [vp, szp]
+        lib.m3_norm_bwd.argtypes = [vp, vp, i64, vp, f32, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp,
+                                    sz, vp]
         lib.m3_query_status.argtypes = [vp, vp]
         lib.m3_status_string.argtypes = [ctypes.c_int]
         lib.m3_status_string.restype = ctypes.c_char_p
@@ -483,6 +480,7 @@ def m3_scan_bwd_ex(dims: Dims, seqlen: int, x, B, C, dt, A, lam, theta, D, state
 # device's current stream unless ``stream`` is given.
 
 _F32 = torch.float32
+_E4M3 = (torch.float8_e4m3fn, torch.uint8)
 _TYPE_OF = {M3_F32: torch.float32, M3_BF16: torch.bfloat16}
 
 
@@ -521,80 +519,102 @@ class NormDims:
         return m3_norm_dims(self.rows, self.width, self.io_dtype, self.res_dtype, self.out)
 
 
-class _Call:
-    """The tensors of one call: checks them against the call's dims, holds their device, and
-    runs the library function there."""
+# A call's structs go to the library as packed bytes, in the layouts of include/m3.h (the ctypes
+# structures above describe them field by field): single-token calls are short, and building
+# ctypes structures would take longer than the kernel.
+_PACK_CONV_DIMS = struct.Struct("4i").pack
+_PACK_SEL_DIMS = struct.Struct("5i").pack
+_PACK_NORM_DIMS = struct.Struct("5i").pack
+_PACK_ROWS = struct.Struct("Pqq").pack
+_PACK_CONV_GRADS = struct.Struct("PqqPPP").pack
+_PACK_SEL_INPUTS = struct.Struct("PqqPqqPqqPqqPqqPPPP").pack
+_PACK_SEL_GRADS = struct.Struct("PqqPqqPqqPqqPqqPPPP").pack
+_NO_ROWS = (0, 0, 0)
 
-    __slots__ = ("name", "device", "lib")
 
-    def __init__(self, name):
-        self.name, self.device, self.lib = name, None, load_library()
+def _bad(status, name, t, what):
+    raise M3Error(status, f"{name}: got {t.dtype} {tuple(t.shape)} on {t.device}, strides "
+                          f"{t.stride()}; expected {what}")
 
-    def _same_device(self, t):
-        if self.device is None:
-            if not t.is_cuda:
-                raise M3Error(M3_ERR_UNSUPPORTED, f"{self.name}: tensors must be on a CUDA device")
-            self.device = t.device
-        elif t.device != self.device:
-            raise M3Error(M3_ERR_UNSUPPORTED, f"{self.name}: tensors on several devices")
 
-    def rows(self, t, lead, width, dtype):
-        """An activation [*lead, *width] (its last axes packed) as m3_rows; lead is (batch,) or
-        (batch, T)."""
-        if t is None:
-            return m3_rows(None, 0, 0)
-        self._same_device(t)
-        if t.dtype != dtype:
-            raise M3Error(M3_ERR_DTYPE, self.name)
-        shape, st, k = t.shape, t.stride(), len(lead)
-        if tuple(shape) != lead + width:
-            raise M3Error(M3_ERR_SHAPE, f"{self.name}: shape {tuple(shape)}, not {lead + width}")
-        packed = 1
-        for n, s in zip(reversed(shape[k:]), reversed(st[k:])):
-            if n > 1 and s != packed:
-                raise M3Error(M3_ERR_SHAPE, f"{self.name}: the last axes must be contiguous")
-            packed *= n
-        return m3_rows(t.data_ptr() or None, st[0], st[1] if k == 2 else 0)
+def _device(t, name):
+    """The index of a call's device: that of its first tensor."""
+    dev = t.get_device()
+    if dev < 0:
+        _bad(M3_ERR_UNSUPPORTED, name, t, "a CUDA tensor")
+    return dev
 
-    def packed(self, t, shape, dtype):
-        """A packed tensor's address (None stays None)."""
-        if t is None:
-            return None
-        self._same_device(t)
-        if t.dtype != dtype:
-            raise M3Error(M3_ERR_DTYPE, self.name)
-        if tuple(t.shape) != shape or not t.is_contiguous():
-            raise M3Error(M3_ERR_SHAPE, f"{self.name}: a packed {shape} tensor is expected")
-        return t.data_ptr() or None
 
-    def matrix(self, t, shape, dtype):
-        """A [rows, width] tensor's address and row stride."""
-        if t is None:
-            return None, 0
-        self._same_device(t)
-        if t.dtype not in dtype:
-            raise M3Error(M3_ERR_DTYPE, self.name)
-        st = t.stride()
-        if tuple(t.shape) != shape or (shape[1] > 1 and st[1] != 1):
-            raise M3Error(M3_ERR_SHAPE, f"{self.name}: a {shape} tensor of packed rows is expected")
-        return t.data_ptr() or None, st[0]
+def _rows(t, shape, lead, dtype, dev, name):
+    """An activation of this shape, whose axes after the first ``lead`` are contiguous, as the
+    fields of an m3_rows: address, batch stride, token stride."""
+    if t is None:
+        return _NO_ROWS
+    if t.dtype is not dtype:
+        _bad(M3_ERR_DTYPE, name, t, dtype)
+    if t.shape != shape:
+        _bad(M3_ERR_SHAPE, name, t, shape)
+    if t.get_device() != dev:
+        _bad(M3_ERR_UNSUPPORTED, name, t, f"device {dev}")
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] != 1:
+        _bad(M3_ERR_SHAPE, name, t, "a contiguous last axis")
+    if len(shape) > lead + 1 and st[lead] != shape[-1] and shape[lead] != 1:
+        _bad(M3_ERR_SHAPE, name, t, "contiguous groups")
+    return t.data_ptr(), st[0], st[1] if lead == 2 else 0
 
-    def workspace(self, t):
-        if t is None:
-            return None, 0
-        self._same_device(t)
-        if not t.is_contiguous():
-            raise M3Error(M3_ERR_WORKSPACE, self.name)
-        return t.data_ptr() or None, t.numel() * t.element_size()
 
-    def run(self, stream, *args):
-        fn = getattr(self.lib, self.name)
-        index = self.device.index
-        if index == torch.cuda.current_device():
-            _check(fn(*args, _stream(stream)), self.name)
-        else:
-            with torch.cuda.device(index):
-                _check(fn(*args, _stream(stream)), self.name)
+def _packed(t, shape, dtype, dev, name):
+    """A packed tensor's address (None: 0)."""
+    if t is None:
+        return 0
+    if t.dtype is not dtype:
+        _bad(M3_ERR_DTYPE, name, t, dtype)
+    if t.shape != shape or not t.is_contiguous():
+        _bad(M3_ERR_SHAPE, name, t, f"packed {shape}")
+    if t.get_device() != dev:
+        _bad(M3_ERR_UNSUPPORTED, name, t, f"device {dev}")
+    return t.data_ptr()
+
+
+def _matrix(t, shape, dtypes, dev, name):
+    """A [rows, width] tensor's address and row stride."""
+    if t is None:
+        return 0, 0
+    if t.dtype not in dtypes:
+        _bad(M3_ERR_DTYPE, name, t, dtypes)
+    st = t.stride()
+    if t.shape != shape or (st[1] != 1 and shape[1] != 1):
+        _bad(M3_ERR_SHAPE, name, t, shape)
+    if t.get_device() != dev:
+        _bad(M3_ERR_UNSUPPORTED, name, t, f"device {dev}")
+    return t.data_ptr(), st[0]
+
+
+def _workspace(t, dev, name):
+    if t is None:
+        return None, 0
+    if not t.is_contiguous():
+        _bad(M3_ERR_WORKSPACE, name, t, "a contiguous workspace")
+    if t.get_device() != dev:
+        _bad(M3_ERR_UNSUPPORTED, name, t, f"device {dev}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def _run(name, dev, stream, *args):
+    """Call the library on device ``dev``: on its current stream, or on ``stream``."""
+    fn = getattr(_lib or load_library(), name)
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if dev == torch._C._cuda_getDevice():
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, stream)
+    if status != M3_OK:
+        raise M3Error(status, name)
 
 
 def _io_type(dims, name):
@@ -604,31 +624,29 @@ def _io_type(dims, name):
     return t
 
 
-def _conv_args(call, dims, lead, x, weight, bias, state, seqlens):
-    io, C, W = _io_type(dims, call.name), dims.channels, dims.width
-    return (call.rows(x, lead, (C,), io), call.packed(weight, (C, W), _F32),
-            call.packed(bias, (C,), _F32), call.packed(seqlens, (dims.batch,), torch.int32),
-            call.packed(state, (dims.batch, W - 1, C), io))
-
-
 def m3_conv_fwd(dims: ConvDims, seqlen: int, x, weight, bias, state, y, seqlens=None,
                 flags: int = 0, stream=None):
     """Short causal convolution of x [b, T, C] into y, carrying ``state`` [b, W-1, C] (updated in
     place).  ``bias`` and ``seqlens`` (int32 [b]) may be None; flags: M3_FLAG_SILU."""
-    call, lead = _Call("m3_conv_fwd"), (dims.batch, seqlen)
-    xr, w, bi, sl, st = _conv_args(call, dims, lead, x, weight, bias, state, seqlens)
-    yr = call.rows(y, lead, (dims.channels,), _io_type(dims, call.name))
-    call.run(stream, ctypes.byref(dims.c()), int(seqlen), ctypes.byref(xr), w, bi, sl, st,
-             ctypes.byref(yr), int(flags))
+    name, b, C, W = "m3_conv_fwd", dims.batch, dims.channels, dims.width
+    io, dev = _io_type(dims, name), _device(x, name)
+    shape = (b, seqlen, C)
+    _run(name, dev, stream, _PACK_CONV_DIMS(b, C, W, dims.io_dtype), seqlen,
+         _PACK_ROWS(*_rows(x, shape, 2, io, dev, name)), _packed(weight, (C, W), _F32, dev, name),
+         _packed(bias, (C,), _F32, dev, name), _packed(seqlens, (b,), torch.int32, dev, name),
+         _packed(state, (b, W - 1, C), io, dev, name),
+         _PACK_ROWS(*_rows(y, shape, 2, io, dev, name)), flags)
 
 
 def m3_conv_step(dims: ConvDims, x, weight, bias, state, y, flags: int = 0, stream=None):
     """One token of every sequence: x, y [b, C]."""
-    call, lead = _Call("m3_conv_step"), (dims.batch,)
-    xr, w, bi, _, st = _conv_args(call, dims, lead, x, weight, bias, state, None)
-    yr = call.rows(y, lead, (dims.channels,), _io_type(dims, call.name))
-    call.run(stream, ctypes.byref(dims.c()), ctypes.byref(xr), w, bi, st, ctypes.byref(yr),
-             int(flags))
+    name, b, C, W = "m3_conv_step", dims.batch, dims.channels, dims.width
+    io, dev = _io_type(dims, name), _device(x, name)
+    shape = (b, C)
+    _run(name, dev, stream, _PACK_CONV_DIMS(b, C, W, dims.io_dtype),
+         _PACK_ROWS(*_rows(x, shape, 1, io, dev, name)), _packed(weight, (C, W), _F32, dev, name),
+         _packed(bias, (C,), _F32, dev, name), _packed(state, (b, W - 1, C), io, dev, name),
+         _PACK_ROWS(*_rows(y, shape, 1, io, dev, name)), flags)
 
 
 def m3_conv_bwd_workspace_bytes(dims: ConvDims, seqlen: int) -> int:
@@ -656,26 +674,31 @@ def m3_conv_bwd(dims: ConvDims, seqlen: int, x, weight, bias, state0, dy, grads:
                 seqlens=None, flags: int = 0, stream=None):
     """Backward of m3_conv_fwd into ``grads`` (see alloc_conv_grads; dbias is needed with a bias,
     dstate may be absent); ``state0`` is the state that the forward call started from."""
-    call, lead = _Call("m3_conv_bwd"), (dims.batch, seqlen)
-    io, C, W = _io_type(dims, call.name), dims.channels, dims.width
-    xr, w, bi, sl, st = _conv_args(call, dims, lead, x, weight, bias, state0, seqlens)
-    dyr = call.rows(dy, lead, (C,), io)
-    g = m3_conv_grads(call.rows(grads.get("dx"), lead, (C,), io),
-                      call.packed(grads.get("dweight"), (C, W), _F32),
-                      call.packed(grads.get("dbias"), (C,), _F32),
-                      call.packed(grads.get("dstate"), (dims.batch, W - 1, C), _F32))
-    ws, nb = call.workspace(workspace)
-    call.run(stream, ctypes.byref(dims.c()), int(seqlen), ctypes.byref(xr), w, bi, sl, st,
-             ctypes.byref(dyr), ctypes.byref(g), ws, nb, int(flags))
+    name, b, C, W = "m3_conv_bwd", dims.batch, dims.channels, dims.width
+    io, dev = _io_type(dims, name), _device(x, name)
+    shape, get = (b, seqlen, C), grads.get
+    _run(name, dev, stream, _PACK_CONV_DIMS(b, C, W, dims.io_dtype), seqlen,
+         _PACK_ROWS(*_rows(x, shape, 2, io, dev, name)), _packed(weight, (C, W), _F32, dev, name),
+         _packed(bias, (C,), _F32, dev, name), _packed(seqlens, (b,), torch.int32, dev, name),
+         _packed(state0, (b, W - 1, C), io, dev, name),
+         _PACK_ROWS(*_rows(dy, shape, 2, io, dev, name)),
+         _PACK_CONV_GRADS(*_rows(get("dx"), shape, 2, io, dev, name),
+                          _packed(get("dweight"), (C, W), _F32, dev, name),
+                          _packed(get("dbias"), (C,), _F32, dev, name),
+                          _packed(get("dstate"), (b, W - 1, C), _F32, dev, name)),
+         *_workspace(workspace, dev, name), flags)
 
 
-def _sel_inputs(call, dims, lead, x, dt, A, B, C, D, z, dt_bias, seqlens):
-    io, ch, gn = _io_type(dims, call.name), (dims.channels,), (dims.ngroups, dims.dstate)
-    return m3_sel_inputs(
-        call.rows(x, lead, ch, io), call.rows(dt, lead, ch, io), call.rows(B, lead, gn, io),
-        call.rows(C, lead, gn, io), call.rows(z, lead, ch, io),
-        call.packed(A, (dims.channels, dims.dstate), _F32), call.packed(D, ch, _F32),
-        call.packed(dt_bias, ch, _F32), call.packed(seqlens, (dims.batch,), torch.int32))
+def _sel_inputs(dims, lead, x, dt, A, B, C, D, z, dt_bias, seqlens, dev, name):
+    """The call's dims and m3_sel_inputs, packed; lead is (b, T) or (b,)."""
+    io, b, ch, G, N = _io_type(dims, name), dims.batch, dims.channels, dims.ngroups, dims.dstate
+    k, wide, gn = len(lead), (*lead, ch), (*lead, G, N)
+    return _PACK_SEL_DIMS(b, ch, G, N, dims.io_dtype), _PACK_SEL_INPUTS(
+        *_rows(x, wide, k, io, dev, name), *_rows(dt, wide, k, io, dev, name),
+        *_rows(B, gn, k, io, dev, name), *_rows(C, gn, k, io, dev, name),
+        *_rows(z, wide, k, io, dev, name), _packed(A, (ch, N), _F32, dev, name),
+        _packed(D, (ch,), _F32, dev, name), _packed(dt_bias, (ch,), _F32, dev, name),
+        _packed(seqlens, (b,), torch.int32, dev, name))
 
 
 def m3_sel_workspace_bytes(dims: SelDims, seqlen: int) -> int:
@@ -694,22 +717,22 @@ def m3_sel_fwd(dims: SelDims, seqlen: int, x, dt, A, B, C, D, z, dt_bias, h, y, 
     """Selective scan of x [b, T, D] into y, carrying h [b, D, N] fp32 (updated in place).
     dt, z like x; B, C [b, T, G, N]; A [D, N] fp32; D, dt_bias [D] fp32.  D, z, dt_bias, seqlens
     (int32 [b]) and workspace may be None; flags: M3_FLAG_DT_SOFTPLUS."""
-    call, lead = _Call("m3_sel_fwd"), (dims.batch, seqlen)
-    inp = _sel_inputs(call, dims, lead, x, dt, A, B, C, D, z, dt_bias, seqlens)
-    yr = call.rows(y, lead, (dims.channels,), _io_type(dims, call.name))
-    hp = call.packed(h, (dims.batch, dims.channels, dims.dstate), _F32)
-    ws, nb = call.workspace(workspace)
-    call.run(stream, ctypes.byref(dims.c()), int(seqlen), ctypes.byref(inp), hp, ctypes.byref(yr),
-             ws, nb, int(flags))
+    name, b, ch = "m3_sel_fwd", dims.batch, dims.channels
+    dev, lead = _device(x, name), (b, seqlen)
+    packed = _sel_inputs(dims, lead, x, dt, A, B, C, D, z, dt_bias, seqlens, dev, name)
+    _run(name, dev, stream, packed[0], seqlen, packed[1],
+         _packed(h, (b, ch, dims.dstate), _F32, dev, name),
+         _PACK_ROWS(*_rows(y, (b, seqlen, ch), 2, _TYPE_OF[dims.io_dtype], dev, name)),
+         *_workspace(workspace, dev, name), flags)
 
 
 def m3_sel_step(dims: SelDims, x, dt, A, B, C, D, z, dt_bias, h, y, flags: int = 0, stream=None):
     """One token of every sequence: x, dt, z, y [b, D]; B, C [b, G, N]."""
-    call, lead = _Call("m3_sel_step"), (dims.batch,)
-    inp = _sel_inputs(call, dims, lead, x, dt, A, B, C, D, z, dt_bias, None)
-    yr = call.rows(y, lead, (dims.channels,), _io_type(dims, call.name))
-    hp = call.packed(h, (dims.batch, dims.channels, dims.dstate), _F32)
-    call.run(stream, ctypes.byref(dims.c()), ctypes.byref(inp), hp, ctypes.byref(yr), int(flags))
+    name, b, ch = "m3_sel_step", dims.batch, dims.channels
+    dev = _device(x, name)
+    packed = _sel_inputs(dims, (b,), x, dt, A, B, C, D, z, dt_bias, None, dev, name)
+    _run(name, dev, stream, *packed, _packed(h, (b, ch, dims.dstate), _F32, dev, name),
+         _PACK_ROWS(*_rows(y, (b, ch), 1, _TYPE_OF[dims.io_dtype], dev, name)), flags)
 
 
 def m3_sel_bwd_workspace_bytes(dims: SelDims, seqlen: int) -> int:
@@ -742,23 +765,20 @@ def m3_sel_bwd(dims: SelDims, seqlen: int, x, dt, A, B, C, D, z, dt_bias, h0, dy
                grads: dict, workspace, seqlens=None, flags: int = 0, stream=None):
     """Backward of m3_sel_fwd into ``grads`` (see alloc_sel_grads; dh may be absent); ``h0`` is
     the state that the forward call started from, ``dhT`` [b, D, N] fp32 may be None."""
-    call, lead = _Call("m3_sel_bwd"), (dims.batch, seqlen)
-    io, ch, gn = _io_type(dims, call.name), (dims.channels,), (dims.ngroups, dims.dstate)
-    hs = (dims.batch, dims.channels, dims.dstate)
-    inp = _sel_inputs(call, dims, lead, x, dt, A, B, C, D, z, dt_bias, seqlens)
-    dyr = call.rows(dy, lead, ch, io)
-    get = grads.get
-    g = m3_sel_grads(
-        call.rows(get("dx"), lead, ch, io), call.rows(get("ddt"), lead, ch, io),
-        call.rows(get("dB"), lead, gn, io), call.rows(get("dC"), lead, gn, io),
-        call.rows(get("dz"), lead, ch, io),
-        call.packed(get("dA"), (dims.channels, dims.dstate), _F32),
-        call.packed(get("dD"), ch, _F32), call.packed(get("ddt_bias"), ch, _F32),
-        call.packed(get("dh"), hs, _F32))
-    ws, nb = call.workspace(workspace)
-    call.run(stream, ctypes.byref(dims.c()), int(seqlen), ctypes.byref(inp),
-             call.packed(h0, hs, _F32), ctypes.byref(dyr), call.packed(dhT, hs, _F32),
-             ctypes.byref(g), ws, nb, int(flags))
+    name, b, ch, G, N = "m3_sel_bwd", dims.batch, dims.channels, dims.ngroups, dims.dstate
+    dev, lead, get = _device(x, name), (b, seqlen), grads.get
+    packed = _sel_inputs(dims, lead, x, dt, A, B, C, D, z, dt_bias, seqlens, dev, name)
+    io, wide, gn, hs = _TYPE_OF[dims.io_dtype], (b, seqlen, ch), (b, seqlen, G, N), (b, ch, N)
+    _run(name, dev, stream, packed[0], seqlen, packed[1], _packed(h0, hs, _F32, dev, name),
+         _PACK_ROWS(*_rows(dy, wide, 2, io, dev, name)), _packed(dhT, hs, _F32, dev, name),
+         _PACK_SEL_GRADS(
+             *_rows(get("dx"), wide, 2, io, dev, name), *_rows(get("ddt"), wide, 2, io, dev, name),
+             *_rows(get("dB"), gn, 2, io, dev, name), *_rows(get("dC"), gn, 2, io, dev, name),
+             *_rows(get("dz"), wide, 2, io, dev, name), _packed(get("dA"), (ch, N), _F32, dev, name),
+             _packed(get("dD"), (ch,), _F32, dev, name),
+             _packed(get("ddt_bias"), (ch,), _F32, dev, name),
+             _packed(get("dh"), hs, _F32, dev, name)),
+         *_workspace(workspace, dev, name), flags)
 
 
 def _norm_types(dims, name):
@@ -777,14 +797,17 @@ def m3_norm_fwd(dims: NormDims, x, residual, weight, eps: float, y, scales=None,
     """r = x + residual (kept in ``residual_out``), y = r / rms(r) * weight.  With M3_OUT_E4M3, y
     is float8_e4m3fn (or uint8) and ``scales`` [rows, ceil(width / 128)] fp32.  residual, weight
     and residual_out may be None."""
-    call, shape = _Call("m3_norm_fwd"), (dims.rows, dims.width)
-    io, res = _norm_types(dims, call.name)
-    q = (torch.float8_e4m3fn, torch.uint8) if dims.out == M3_OUT_E4M3 else io
-    args = (*call.matrix(x, shape, io), *call.matrix(residual, shape, res),
-            call.packed(weight, (dims.width,), _F32), float(eps), *call.matrix(y, shape, q),
-            call.packed(scales, (dims.rows, (dims.width + 127) // 128), _F32),
-            *call.matrix(residual_out, shape, res))
-    call.run(stream, ctypes.byref(dims.c()), *args)
+    name, rows, width = "m3_norm_fwd", dims.rows, dims.width
+    io, res = _norm_types(dims, name)
+    dev, shape = _device(x, name), (rows, width)
+    e4m3 = dims.out == M3_OUT_E4M3
+    _run(name, dev, stream,
+         _PACK_NORM_DIMS(rows, width, dims.io_dtype, dims.res_dtype, dims.out),
+         *_matrix(x, shape, io, dev, name), *_matrix(residual, shape, res, dev, name),
+         _packed(weight, (width,), _F32, dev, name), eps,
+         *_matrix(y, shape, _E4M3 if e4m3 else io, dev, name),
+         _packed(scales, (rows, (width + 127) // 128), _F32, dev, name),
+         *_matrix(residual_out, shape, res, dev, name))
 
 
 def m3_norm_bwd_workspace_bytes(dims: NormDims) -> int:
@@ -803,10 +826,12 @@ def m3_norm_bwd(dims: NormDims, r, weight, eps: float, dy, dres, dx, dresidual, 
     """Backward of m3_norm_fwd: ``r`` is its residual_out (x without a residual), ``dres`` the
     gradient of residual_out or None.  dr goes to ``dx`` in the io type and to ``dresidual``
     (None: not wanted) in the residual's."""
-    call, shape = _Call("m3_norm_bwd"), (dims.rows, dims.width)
-    io, res = _norm_types(dims, call.name)
-    args = (*call.matrix(r, shape, res), call.packed(weight, (dims.width,), _F32), float(eps),
-            *call.matrix(dy, shape, io), *call.matrix(dres, shape, res),
-            *call.matrix(dx, shape, io), *call.matrix(dresidual, shape, res),
-            call.packed(dweight, (dims.width,), _F32), *call.workspace(workspace))
-    call.run(stream, ctypes.byref(dims.c()), *args)
+    name, rows, width = "m3_norm_bwd", dims.rows, dims.width
+    io, res = _norm_types(dims, name)
+    dev, shape = _device(dy, name), (rows, width)
+    _run(name, dev, stream,
+         _PACK_NORM_DIMS(rows, width, dims.io_dtype, dims.res_dtype, dims.out),
+         *_matrix(r, shape, res, dev, name), _packed(weight, (width,), _F32, dev, name), eps,
+         *_matrix(dy, shape, io, dev, name), *_matrix(dres, shape, res, dev, name),
+         *_matrix(dx, shape, io, dev, name), *_matrix(dresidual, shape, res, dev, name),
+         _packed(dweight, (width,), _F32, dev, name), *_workspace(workspace, dev, name))
