@@ -264,13 +264,15 @@ void sel_args(SelArgs* a, const m3_sel_dims* d, int32_t T, const m3_sel_inputs* 
     a->softplus = flags & M3_FLAG_DT_SOFTPLUS;
 }
 
-// Whether every row of x, dt, z, B and C, and every group's part of it, starts on 16 bytes and
-// is a multiple of 16 bytes long: tiles then come by asynchronous 16-byte copies.
+// Whether every row of x, dt and z, and every group's part of it, starts on 16 bytes and is a
+// multiple of 16 bytes long: tiles then come by asynchronous 16-byte copies.
 bool sel_wide(const m3_sel_dims* d, const Geo& g, const m3_sel_inputs* in) {
-    const int per = 16 / (int)g.e;
-    return d->channels / d->ngroups % per == 0 && d->dstate % per == 0 && wide_rows(in->x, g) &&
-           wide_rows(in->dt, g) && (!in->z.ptr || wide_rows(in->z, g)) && wide_rows(in->B, g) &&
-           wide_rows(in->C, g);
+    return d->channels / d->ngroups % (16 / (int)g.e) == 0 && wide_rows(in->x, g) &&
+           wide_rows(in->dt, g) && (!in->z.ptr || wide_rows(in->z, g));
+}
+// The same of B and C.
+bool sel_wide_bc(const m3_sel_dims* d, const Geo& g, const m3_sel_inputs* in) {
+    return d->dstate % (16 / (int)g.e) == 0 && wide_rows(in->B, g) && wide_rows(in->C, g);
 }
 
 // An upper bound of the blocks of any launch over (tile, segment, batch) or over the states.
@@ -311,6 +313,7 @@ m3_status m3_sel_fwd(const m3_sel_dims* d, int32_t T, const m3_sel_inputs* in, f
     sel_args(&a, d, T, in, h, flags);
     set_out(a.y, *y);
     a.wide = sel_wide(d, g, in) && wide_rows(*y, g);
+    a.wide_bc = sel_wide_bc(d, g, in);
     a.nseg = sel_fwd_segments(a.batch, T, a.D, a.G, a.N, &a.seg);
     if (a.nseg > 1 && (!ws || ws_bytes < sel_fwd_workspace(a.batch, T, a.D, a.G, a.N))) a.nseg = 1;
     if (a.nseg == 1) a.seg = T;
@@ -475,7 +478,7 @@ m3_status m3_norm_bwd_workspace_bytes(const m3_norm_dims* d, size_t* bytes) {
     m3_status st = norm_dims_ok(d);
     if (st != M3_OK) return st;
     if (!bytes) return M3_ERR_NULL;
-    const size_t n = sizeof(float) * norm_bwd_shares(d->rows, d->width) * d->width;
+    const size_t n = sizeof(float) * (size_t)norm_bwd_blocks(d->rows, d->width) * d->width;
     *bytes = n < 256 ? 256 : (n + 255) / 256 * 256;
     return M3_OK;
 }

@@ -183,4 +183,23 @@ __device__ __forceinline__ int lane_sum(float (&v)[K], int lane) {
     }
 }
 
+// Sum of a column of shares, p[r * stride] for r < rows, by a block of 1024 threads of which lane
+// l of every warp passes the same column: each warp takes every 32nd row, then the warps' sums add
+// up in order.  The result is valid in the first warp.
+__device__ __forceinline__ float column_sum(const float* p, int rows, long long stride, bool on) {
+    __shared__ float sm[32][33];
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    float s = 0.f;
+    if (on)
+#pragma unroll 8
+        for (int r = wid; r < rows; r += 32) s += p[r * stride];
+    sm[wid][lane] = s;
+    __syncthreads();
+    float v = 0.f;
+    if (wid == 0)
+#pragma unroll
+        for (int i = 0; i < 32; i++) v += sm[i][lane];
+    return v;
+}
+
 }  // namespace m3

@@ -57,7 +57,10 @@ struct SelArgs {
     int batch, T, D, G, N;
     int seg, nseg;         // tokens per segment (a multiple of the tile), segments
     int tile, ntile;       // backward: tokens per tile, tiles
-    bool softplus, wide, step_rows;
+    bool softplus;
+    bool wide;             // rows of channels: 16-byte copies, pairs of channels in one access
+    bool wide_bc;          // the same of B and C (forward)
+    bool step_rows;
 };
 // Tokens of one staged tile: segments are multiples of it.
 constexpr int kSelTile = 32;
@@ -83,7 +86,6 @@ struct NormArgs {
     bool wide;
 };
 int norm_bwd_blocks(int rows, int d);
-size_t norm_bwd_shares(int rows, int d);
 cudaError_t launch_norm_fwd(const NormArgs& a, int io_dtype, int res_dtype, int out, cudaStream_t s);
 cudaError_t launch_norm_bwd(const NormArgs& a, int io_dtype, int res_dtype, cudaStream_t s);
 

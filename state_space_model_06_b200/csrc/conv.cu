@@ -391,23 +391,12 @@ __global__ void __launch_bounds__(128, W <= 4 ? 4 : 2) conv_bwd_kernel(const Con
     }
 }
 
-// Sums the shares over the runs, in a fixed order: a block per 32 channels and tap, its warps
-// taking every eighth run each.
-__global__ void __launch_bounds__(256) conv_bwd_sum_kernel(const float* part, int runs, int W, int C,
-                                                           float* dweight, float* dbias) {
-    __shared__ float sm[8][33];
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + lane, k = blockIdx.y;
-    float s = 0.f;
-    if (c < C)
-#pragma unroll 4
-        for (int r = wid; r < runs; r += 8) s += part[((long long)r * (W + 1) + k) * C + c];
-    sm[wid][lane] = s;
-    __syncthreads();
-    if (wid == 0 && c < C) {
-        float v = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; i++) v += sm[i][lane];
+// Sums the shares over the runs: a block per 32 channels and tap (the last one is the bias).
+__global__ void __launch_bounds__(1024) conv_bwd_sum_kernel(const float* part, int runs, int W, int C,
+                                                            float* dweight, float* dbias) {
+    const int c = blockIdx.x * 32 + (threadIdx.x & 31), k = blockIdx.y;
+    const float v = column_sum(part + (long long)k * C + c, runs, (long long)(W + 1) * C, c < C);
+    if (threadIdx.x < 32 && c < C) {
         if (k < W)
             dweight[(long long)c * W + k] = v;
         else if (dbias)
@@ -433,7 +422,7 @@ template <typename IO, int W, bool WIDE>
 cudaError_t bwd_t(const ConvArgs& a, cudaStream_t s) {
     const dim3 grid(a.batch * a.nseg, (a.C + 128 * V - 1) / (128 * V));
     conv_bwd_kernel<IO, W, WIDE><<<grid, 128, 0, s>>>(a);
-    conv_bwd_sum_kernel<<<dim3((a.C + 31) / 32, W + 1), 256, 0, s>>>(
+    conv_bwd_sum_kernel<<<dim3((a.C + 31) / 32, W + 1), 1024, 0, s>>>(
         a.part, a.batch * a.nseg, W, a.C, a.dweight, a.dbias);
     return cudaGetLastError();
 }

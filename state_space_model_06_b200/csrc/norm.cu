@@ -221,8 +221,21 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_bwd_kernel(const N
         }
     }
     if (a.part) {
-        // the row groups of a block have a row of shares each
-        float* o = a.part + ((long long)blockIdx.x * RPB + threadIdx.x / TPR) * a.d;
+        float* o = a.part + (long long)blockIdx.x * a.d;
+        if constexpr (RPB > 1) {
+            // the row groups of a block add up, in order
+            __shared__ float sums[RPB][TPR][9];
+#pragma unroll
+            for (int j = 0; j < 8; j++) sums[threadIdx.x / TPR][k][j] = dw[0][j];
+            __syncthreads();
+            if (threadIdx.x >= TPR) return;
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                dw[0][j] = 0.f;
+#pragma unroll
+                for (int g = 0; g < RPB; g++) dw[0][j] += sums[g][k][j];
+            }
+        }
 #pragma unroll
         for (int v = 0; v < NV; v++) {
             const int i = (k + v * TPR) * 8;
@@ -231,23 +244,11 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_bwd_kernel(const N
     }
 }
 
-__global__ void __launch_bounds__(256) norm_bwd_sum_kernel(const float* part, int shares, int d,
-                                                           float* dweight) {
-    __shared__ float sm[8][33];
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + lane;
-    float s = 0.f;
-    if (c < d)
-#pragma unroll 8
-        for (int r = wid; r < shares; r += 8) s += part[(long long)r * d + c];
-    sm[wid][lane] = s;
-    __syncthreads();
-    if (wid == 0 && c < d) {
-        float v = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; i++) v += sm[i][lane];
-        dweight[c] = v;
-    }
+__global__ void __launch_bounds__(1024) norm_bwd_sum_kernel(const float* part, int shares, int d,
+                                                            float* dweight) {
+    const int c = blockIdx.x * 32 + (threadIdx.x & 31);
+    const float v = column_sum(part + c, shares, d, c < d);
+    if (threadIdx.x < 32 && c < d) dweight[c] = v;
 }
 
 // Threads of a row: the fewest that hold it with two vectors each (1024 hold four).
@@ -287,8 +288,7 @@ cudaError_t bwd_t(const NormArgs& a, cudaStream_t s) {
     auto go = [&](auto kernel, int tpr) {
         kernel<<<a.blocks, tpr < 128 ? 128 : tpr, 0, s>>>(a);
         if (a.part) {
-            const int rpb = tpr < 128 ? 128 / tpr : 1;
-            norm_bwd_sum_kernel<<<(a.d + 31) / 32, 256, 0, s>>>(a.part, a.blocks * rpb, a.d, a.dweight);
+            norm_bwd_sum_kernel<<<(a.d + 31) / 32, 1024, 0, s>>>(a.part, a.blocks, a.d, a.dweight);
         }
         return cudaGetLastError();
     };
@@ -321,11 +321,6 @@ int norm_bwd_blocks(int rows, int d) {
     const long long groups = ((long long)rows + rpb - 1) / rpb;
     const int most = 148 * (1024 / threads);
     return (int)(groups < most ? (groups < 1 ? 1 : groups) : most);
-}
-
-size_t norm_bwd_shares(int rows, int d) {
-    const int tpr = bwd_threads(d), rpb = tpr < 128 ? 128 / tpr : 1;
-    return (size_t)norm_bwd_blocks(rows, d) * rpb;
 }
 
 cudaError_t launch_norm_fwd(const NormArgs& a, int io, int res, int out, cudaStream_t s) {

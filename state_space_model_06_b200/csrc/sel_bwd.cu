@@ -286,10 +286,14 @@ __global__ void __launch_bounds__(SH::THREADS, SH::MIN_BLOCKS) sel_bwd_kernel(co
     f2 lam[2][NT / 2], A2[2][NT / 2], dA[2][NT / 2];
     float skip[2] = {0.f, 0.f}, bias[2] = {0.f, 0.f}, dD[2] = {0.f, 0.f}, dbias[2] = {0.f, 0.f};
     const long long row = (((long long)p.b * a.nseg + p.seg) * a.D + c) * a.N;
+    // a sequence of one tile is not chained: it starts from h0 and dhT (row is theirs then)
+    const bool single = a.ntile == 1;
+    const float* entry = single ? a.h : a.hseg;
+    const float* leaving = single ? a.dhT : a.gseg;
 #pragma unroll
     for (int q = 0; q < 2; q++) {
         row_pairs<NT>(A2[q], a.A + (long long)(c + q) * a.N, q < mine, s * NT, a.N, kLog2e);
-        row_pairs<NT>(lam[q], a.gseg + row + q * a.N, q < mine, s * NT, a.N, 1.f);
+        row_pairs<NT>(lam[q], leaving + row + q * a.N, q < mine && leaving, s * NT, a.N, 1.f);
 #pragma unroll
         for (int i = 0; i < NT / 2; i++) dA[q][i] = 0;
         if (q < mine && a.Dskip) skip[q] = a.Dskip[c + q];
@@ -306,7 +310,7 @@ __global__ void __launch_bounds__(SH::THREADS, SH::MIN_BLOCKS) sel_bwd_kernel(co
         f2 h[2][NT / 2];
 #pragma unroll
         for (int q = 0; q < 2; q++) {
-            row_pairs<NT>(h[q], a.hseg + row + q * a.N, q < mine, s * NT, a.N, 1.f);
+            row_pairs<NT>(h[q], entry + row + q * a.N, q < mine, s * NT, a.N, 1.f);
             if (jt > 0) {
                 // decayed from the segment's entry, plus the segment's own
                 const long long k = (long long)p.b * a.ntile + p.seg * tiles + jt - 1;
@@ -503,6 +507,7 @@ __global__ void __launch_bounds__(SH::THREADS, SH::MIN_BLOCKS) sel_bwd_kernel(co
             dbias[q] += __shfl_xor_sync(0xffffffffu, dbias[q], o);
         }
         store_pairs<NT>(dA[q], a.pA + row + q * a.N, q < mine, s * NT, a.N);
+        if (single && a.dh) store_pairs<NT>(lam[q], a.dh + row + q * a.N, q < mine, s * NT, a.N);
         if (q < mine && s == 0) {
             float* o = a.pD + ((long long)p.b * a.nseg + p.seg) * 2 * a.D + c + q;
             o[0] = dD[q];
@@ -538,25 +543,13 @@ __global__ void __launch_bounds__(256) sel_bwd_bc_kernel(const SelArgs a, int NP
         static_cast<IO*>(a.dB.p)[b * a.dB.bs + t * a.dB.ts + at] = from_f<IO>(v);
 }
 
-// Column sums of the segments' shares: dA ([runs][D N]), then dD and ddt_bias ([runs][2][D]).  A
-// block per 32 columns, a warp every eighth run.
-__global__ void __launch_bounds__(256) sel_bwd_sum_kernel(const SelArgs a) {
-    __shared__ float sm[8][33];
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, runs = a.batch * a.nseg;
-    const long long states = (long long)a.D * a.N, c = blockIdx.x * 32ll + lane;
+// Sums of the segments' shares: dA ([runs][D N]), then dD and ddt_bias ([runs][2][D]).
+__global__ void __launch_bounds__(1024) sel_bwd_sum_kernel(const SelArgs a) {
+    const long long states = (long long)a.D * a.N, c = blockIdx.x * 32ll + (threadIdx.x & 31);
     const bool in_A = c < states, on = c < states + 2 * a.D;
-    const float* part = in_A ? a.pA + c : a.pD + (c - states);
-    const long long stride = in_A ? states : 2ll * a.D;
-    float s = 0.f;
-    if (on)
-#pragma unroll 4
-        for (int r = wid; r < runs; r += 8) s += part[r * stride];
-    sm[wid][lane] = s;
-    __syncthreads();
-    if (wid == 0 && on) {
-        float v = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; i++) v += sm[i][lane];
+    const float v = column_sum(in_A ? a.pA + c : a.pD + (c - states), a.batch * a.nseg,
+                               in_A ? states : 2ll * a.D, on);
+    if (threadIdx.x < 32 && on) {
         if (in_A)
             a.dA[c] = v;
         else if (c < states + a.D) {
@@ -573,14 +566,16 @@ cudaError_t bwd_w(const SelArgs& a, cudaStream_t s) {
     cudaError_t e = allow_smem(sel_bwd_local_kernel<IO, SH, WIDE>, SH::LOCAL_BYTES);
     if (e == cudaSuccess) e = allow_smem(sel_bwd_kernel<IO, SH, WIDE>, SH::BYTES);
     if (e != cudaSuccess) return e;
-    sel_bwd_local_kernel<IO, SH, WIDE><<<grid, SH::THREADS, SH::LOCAL_BYTES, s>>>(a);
     const long long states = (long long)a.D * a.N;
-    const int blocks = (int)((states * a.batch + 127) / 128);
-    sel_bwd_chain_kernel<<<2 * blocks, 128, 0, s>>>(a, blocks);
+    if (a.ntile > 1) {
+        sel_bwd_local_kernel<IO, SH, WIDE><<<grid, SH::THREADS, SH::LOCAL_BYTES, s>>>(a);
+        const int blocks = (int)((states * a.batch + 127) / 128);
+        sel_bwd_chain_kernel<<<2 * blocks, 128, 0, s>>>(a, blocks);
+    }
     sel_bwd_kernel<IO, SH, WIDE><<<grid, SH::THREADS, SH::BYTES, s>>>(a);
     const long long bc = (long long)a.batch * a.T * a.G * 2 * a.N;
     sel_bwd_bc_kernel<IO><<<(unsigned)((bc + 255) / 256), 256, 0, s>>>(a, SH::NP, tiles);
-    sel_bwd_sum_kernel<<<(unsigned)((states + 2 * a.D + 31) / 32), 256, 0, s>>>(a);
+    sel_bwd_sum_kernel<<<(unsigned)((states + 2 * a.D + 31) / 32), 1024, 0, s>>>(a);
     return cudaGetLastError();
 }
 
@@ -592,8 +587,8 @@ cudaError_t bwd_t(const SelArgs& a, cudaStream_t s) {
 // The lane shape by the number of states.
 template <typename F>
 cudaError_t by_n(int N, F f) {
-    if (N <= 4) return f(BwdShape<4, 1, 2, 32, 4>{});
-    if (N <= 8) return f(BwdShape<4, 2, 2, 32, 4>{});
+    if (N <= 4) return f(BwdShape<2, 2, 2, 32, 4>{});
+    if (N <= 8) return f(BwdShape<2, 4, 4, 32, 4>{});
     if (N <= 16) return f(BwdShape<4, 4, 4, 32, 4>{});
     if (N <= 32) return f(BwdShape<4, 8, 4, 32, 4>{});
     if (N <= 64) return f(BwdShape<4, 16, 4, 32, 4>{});

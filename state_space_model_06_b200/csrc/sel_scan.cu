@@ -61,9 +61,15 @@ __global__ void __launch_bounds__(SH::THREADS) sel_scan_kernel(const SelArgs a) 
         stage_rows<IO, WIDE, L, CB, THREADS>(&r.dt[0][0], a.dt, p.b, p.c0, t0, end, p.nc);
         if (!LOCAL && a.z.p)
             stage_rows<IO, WIDE, L, CB, THREADS>(&r.z[0][0], a.z, p.b, p.c0, t0, end, p.nc);
-        stage_rows<IO, WIDE, L, Smem::NR, THREADS>(&r.B[0][0], a.B, p.b, bn, t0, end, a.N);
-        if (!LOCAL)
-            stage_rows<IO, WIDE, L, Smem::NR, THREADS>(&r.C[0][0], a.C, p.b, bn, t0, end, a.N);
+        if (WIDE && a.wide_bc) {
+            stage_rows<IO, true, L, Smem::NR, THREADS>(&r.B[0][0], a.B, p.b, bn, t0, end, a.N);
+            if (!LOCAL)
+                stage_rows<IO, true, L, Smem::NR, THREADS>(&r.C[0][0], a.C, p.b, bn, t0, end, a.N);
+        } else {
+            stage_rows<IO, false, L, Smem::NR, THREADS>(&r.B[0][0], a.B, p.b, bn, t0, end, a.N);
+            if (!LOCAL)
+                stage_rows<IO, false, L, Smem::NR, THREADS>(&r.C[0][0], a.C, p.b, bn, t0, end, a.N);
+        }
     };
     if (p.t0 < end) request(p.t0, sm.raw[0]);
     cp_async_commit();
@@ -225,20 +231,31 @@ __global__ void __launch_bounds__(SH::THREADS) sel_scan_kernel(const SelArgs a) 
 }
 
 // Chains the segments: entry state of segment k + 1 = e^{A sum delta_k} (entry of k) + own end of k.
-__global__ void __launch_bounds__(256) sel_chain_kernel(const SelArgs a) {
+__global__ void __launch_bounds__(128) sel_chain_kernel(const SelArgs a) {
     const long long per = (long long)a.D * a.N;
-    const long long i = blockIdx.x * 256ll + threadIdx.x;
+    const long long i = blockIdx.x * 128ll + threadIdx.x;
     if (i >= per * a.batch) return;
     const int b = (int)(i / per);
     const long long dn = i - b * per;
-    const int d = (int)(dn / a.N);
     const float A2 = a.A[dn] * kLog2e;
+    float* hs = a.hseg + (long long)b * a.nseg * per + dn;
+    const float* ds = a.dsum + (long long)b * a.nseg * a.D + (int)(dn / a.N);
+    constexpr int U = 8;          // segments requested together
     float h = a.h[i];
-    for (int k = 0; k < a.nseg; k++) {
-        float* at = a.hseg + ((long long)b * a.nseg + k) * per + dn;
-        const float own = *at;
-        *at = h;
-        h = fmaf(ex2(A2 * a.dsum[((long long)b * a.nseg + k) * a.D + d]), h, own);
+    for (int k0 = 0; k0 < a.nseg; k0 += U) {
+        float own[U], dec[U];
+#pragma unroll
+        for (int u = 0; u < U; u++)
+            if (k0 + u < a.nseg) {
+                own[u] = hs[(k0 + u) * per];
+                dec[u] = ds[(long long)(k0 + u) * a.D];
+            }
+#pragma unroll
+        for (int u = 0; u < U; u++)
+            if (k0 + u < a.nseg) {
+                hs[(k0 + u) * per] = h;
+                h = fmaf(ex2(A2 * dec[u]), h, own[u]);
+            }
     }
 }
 
@@ -387,7 +404,7 @@ cudaError_t fwd_w(const SelArgs& a, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         sel_scan_kernel<IO, SH, WIDE, true><<<grid, SH::THREADS, bytes, s>>>(a);
         const long long n = (long long)a.batch * a.D * a.N;
-        sel_chain_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(a);
+        sel_chain_kernel<<<(unsigned)((n + 127) / 128), 128, 0, s>>>(a);
     }
     sel_scan_kernel<IO, SH, WIDE, false><<<grid, SH::THREADS, bytes, s>>>(a);
     return cudaGetLastError();
@@ -401,8 +418,8 @@ cudaError_t fwd_t(const SelArgs& a, cudaStream_t s) {
 // The lane shape of a forward call, by the number of states.
 template <typename F>
 auto fwd_shape(int N, F f) {
-    if (N <= 4) return f(SelShape<4, 1, 2, 16>{});
-    if (N <= 8) return f(SelShape<4, 2, 2, 32>{});
+    if (N <= 4) return f(SelShape<2, 2, 2, 32>{});
+    if (N <= 8) return f(SelShape<2, 4, 4, 32>{});
     if (N <= 16) return f(SelShape<2, 8, 4, 32, 2>{});
     if (N <= 32) return f(SelShape<4, 8, 4, 32>{});
     if (N <= 64) return f(SelShape<8, 8, 4, 32>{});
