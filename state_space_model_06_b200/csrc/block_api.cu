@@ -406,6 +406,7 @@ m3_status m3_sel_bwd(const m3_sel_dims* d, int32_t T, const m3_sel_inputs* in, c
     set_out(a.dz, gr->dz);
     a.wide = sel_wide(d, g, in) && wide_rows(*dy, g) && wide_rows(gr->dx, g) &&
              wide_rows(gr->ddt, g) && (!in->z.ptr || wide_rows(gr->dz, g));
+    a.wide_bc = sel_wide_bc(d, g, in);
     a.dhT = dhT;
     a.dA = gr->dA;
     a.dD = in->D ? gr->dD : nullptr;

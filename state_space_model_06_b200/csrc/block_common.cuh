@@ -100,6 +100,13 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src, bool on) 
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(d), "l"(src), "r"(bytes)
                  : "memory");
 }
+// The same of 4 bytes.
+__device__ __forceinline__ void cp_async4(void* dst, const void* src, bool on) {
+    const uint32_t d = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    const int bytes = on ? 4 : 0;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d), "l"(src), "r"(bytes)
+                 : "memory");
+}
 // N = 8 or 16 bytes.
 template <int N>
 __device__ __forceinline__ void cp_async(void* dst, const void* src) {
@@ -183,23 +190,24 @@ __device__ __forceinline__ int lane_sum(float (&v)[K], int lane) {
     }
 }
 
-// Sum of a column of shares, p[r * stride] for r < rows, by a block of 1024 threads of which lane
-// l of every warp passes the same column: each warp takes every 32nd row, then the warps' sums add
-// up in order.  The result is valid in the first warp.
+// Sum of a column of shares, p[r * stride] for r < rows, by a block of which lane l of every warp
+// passes the same column: each warp takes every so many rows, then the warps' sums add up in
+// order.  The result is valid in the first warp.
 __device__ __forceinline__ float column_sum(const float* p, int rows, long long stride, bool on) {
     __shared__ float sm[32][33];
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, warps = blockDim.x >> 5;
     float s = 0.f;
     if (on)
 #pragma unroll 8
-        for (int r = wid; r < rows; r += 32) s += p[r * stride];
+        for (int r = wid; r < rows; r += warps) s += p[r * stride];
     sm[wid][lane] = s;
     __syncthreads();
     float v = 0.f;
     if (wid == 0)
-#pragma unroll
-        for (int i = 0; i < 32; i++) v += sm[i][lane];
+        for (int i = 0; i < warps; i++) v += sm[i][lane];
     return v;
 }
+// Threads of such a block: eight warps where the columns alone fill the GPU, else 32.
+inline int column_threads(long long columns) { return columns >= 32 * 148 * 4 ? 256 : 1024; }
 
 }  // namespace m3

@@ -422,7 +422,7 @@ template <typename IO, int W, bool WIDE>
 cudaError_t bwd_t(const ConvArgs& a, cudaStream_t s) {
     const dim3 grid(a.batch * a.nseg, (a.C + 128 * V - 1) / (128 * V));
     conv_bwd_kernel<IO, W, WIDE><<<grid, 128, 0, s>>>(a);
-    conv_bwd_sum_kernel<<<dim3((a.C + 31) / 32, W + 1), 1024, 0, s>>>(
+    conv_bwd_sum_kernel<<<dim3((a.C + 31) / 32, W + 1), column_threads((long long)a.C * (W + 1)), 0, s>>>(
         a.part, a.batch * a.nseg, W, a.C, a.dweight, a.dbias);
     return cudaGetLastError();
 }

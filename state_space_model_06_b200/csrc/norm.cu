@@ -288,7 +288,7 @@ cudaError_t bwd_t(const NormArgs& a, cudaStream_t s) {
     auto go = [&](auto kernel, int tpr) {
         kernel<<<a.blocks, tpr < 128 ? 128 : tpr, 0, s>>>(a);
         if (a.part) {
-            norm_bwd_sum_kernel<<<(a.d + 31) / 32, 1024, 0, s>>>(a.part, a.blocks, a.d, a.dweight);
+            norm_bwd_sum_kernel<<<(a.d + 31) / 32, column_threads(a.d), 0, s>>>(a.part, a.blocks, a.d, a.dweight);
         }
         return cudaGetLastError();
     };

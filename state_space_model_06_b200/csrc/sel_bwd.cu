@@ -43,12 +43,23 @@ struct BwdShape {
     static constexpr int O_BC = 0;                              // [L][2][NP]
     static constexpr int O_DD = O_BC + L * 2 * NP;              // [L][PB] float4: delta, delta x of two channels
     static constexpr int O_E = O_DD + L * PB * 4;               // [L][PB] float2: e
-    static constexpr int O_CK = O_E + L * PB * 2;               // [L / K][CB][NP]
-    static constexpr int O_RED = O_CK + L / K * CB * NP;        // [WARPS][K][2 NP]
-    static constexpr int LOCAL_BYTES = 4 * O_CK;
-    static constexpr int RED = WARPS * K * 2 * NP;              // twice: of a piece and the one before
-    static constexpr int BYTES = 4 * (O_RED + 2 * RED);
-    static_assert(BYTES <= 227 * 1024 && THREADS % PB == 0, "");
+    static constexpr int O_RAW = O_E + L * PB * 2;              // the next tile's rows, as they are
+    static constexpr int RED = WARPS * K * 2 * NP;              // sums over channels, of a piece and the one before
+    static constexpr int KEPT = L / K > 2 ? L / K - 2 : 1;      // states before pieces 1 .. L / K - 2
+    template <typename IO>
+    struct Raw {
+        static constexpr int NR = (NP * (int)sizeof(IO) + 15) / 16 * 16 / (int)sizeof(IO);
+        alignas(16) IO x[L][CB], dt[L][CB], z[L][CB], dy[L][CB], B[L][NR], C[L][NR];
+    };
+    template <typename IO>
+    static constexpr int O_CK = O_RAW + (int)sizeof(Raw<IO>) / 4;              // [KEPT][2][PB][NP]
+    template <typename IO>
+    static constexpr int O_RED = O_CK<IO> + KEPT * CB * NP;                    // [2][WARPS][K][2 NP]
+    template <typename IO>
+    static constexpr int LOCAL_BYTES = 4 * O_CK<IO>;
+    template <typename IO>
+    static constexpr int BYTES = 4 * (O_RED<IO> + 2 * RED);
+    static_assert(THREADS % PB == 0, "");
 };
 
 // Two neighbouring values of a row, as they are (`two` false: the second is not there).
@@ -80,55 +91,65 @@ __device__ __forceinline__ Two<IO> load_two(const IO* p, bool two) {
     return r;
 }
 
-// delta, delta x and e = dy SiLU(z) of a tile's tokens (zero past the end), and B and C
+// Asks for the rows of a tile (with wide rows they arrive while other work goes on).
 template <typename IO, typename SH, bool WIDE>
-__device__ __forceinline__ void bwd_stage(const SelArgs& a, const SelPlace& p, int t0, int end,
-                                          float* sm) {
-    constexpr int PB = SH::PB, STEP = SH::THREADS / PB;
-    constexpr int U = SH::L / STEP < 4 ? SH::L / STEP : 4;      // tokens requested together
-    static_assert(U > 0 && SH::L % (STEP * U) == 0, "");
-    sel_stage_bc<IO, SH::NP, SH::L, SH::THREADS>(a, p, t0, end, sm + SH::O_BC);
-    const int k = threadIdx.x % PB, c = p.c0 + 2 * k;
-    const bool one = 2 * k < p.nc, two = 2 * k + 1 < p.nc;
-    const float2 bias = make_float2(one && a.dt_bias ? a.dt_bias[c] : 0.f,
-                                    two && a.dt_bias ? a.dt_bias[c + 1] : 0.f);
-    const IO* x = static_cast<const IO*>(a.x.p) + p.b * a.x.bs + c;
-    const IO* dt = static_cast<const IO*>(a.dt.p) + p.b * a.dt.bs + c;
-    const IO* z = static_cast<const IO*>(a.z.p) + p.b * a.z.bs + c;
-    const IO* dy = static_cast<const IO*>(a.dy.p) + p.b * a.dy.bs + c;
-#pragma unroll 1
-    for (int u0 = threadIdx.x / PB; u0 < SH::L; u0 += STEP * U) {
-        Two<IO> rx[U], rt[U], rz[U], ry[U];
-#pragma unroll
-        for (int i = 0; i < U; i++) {
-            const long long t = t0 + u0 + i * STEP;
-            if (t < end && one) {
-                rx[i] = load_two<IO, WIDE>(x + t * a.x.ts, two);
-                rt[i] = load_two<IO, WIDE>(dt + t * a.dt.ts, two);
-                ry[i] = load_two<IO, WIDE>(dy + t * a.dy.ts, two);
-                if (a.z.p) rz[i] = load_two<IO, WIDE>(z + t * a.z.ts, two);
+__device__ __forceinline__ void bwd_request(const SelArgs& a, const SelPlace& p, int t0, int end, float* sm) {
+    using Raw = typename SH::template Raw<IO>;
+    Raw& r = *reinterpret_cast<Raw*>(sm + SH::O_RAW);
+    constexpr int L = SH::L, CB = SH::CB, TH = SH::THREADS;
+    const long long bn = (long long)p.g * a.N;
+    stage_rows<IO, WIDE, L, CB, TH>(&r.x[0][0], a.x, p.b, p.c0, t0, end, p.nc);
+    stage_rows<IO, WIDE, L, CB, TH>(&r.dt[0][0], a.dt, p.b, p.c0, t0, end, p.nc);
+    stage_rows<IO, WIDE, L, CB, TH>(&r.dy[0][0], a.dy, p.b, p.c0, t0, end, p.nc);
+    if (a.z.p) stage_rows<IO, WIDE, L, CB, TH>(&r.z[0][0], a.z, p.b, p.c0, t0, end, p.nc);
+    if (WIDE && a.wide_bc) {
+        stage_rows<IO, true, L, Raw::NR, TH>(&r.B[0][0], a.B, p.b, bn, t0, end, a.N);
+        stage_rows<IO, true, L, Raw::NR, TH>(&r.C[0][0], a.C, p.b, bn, t0, end, a.N);
+    } else {
+        stage_rows<IO, false, L, Raw::NR, TH>(&r.B[0][0], a.B, p.b, bn, t0, end, a.N);
+        stage_rows<IO, false, L, Raw::NR, TH>(&r.C[0][0], a.C, p.b, bn, t0, end, a.N);
+    }
+    cp_async_commit();
+}
+
+// delta, delta x and e = dy SiLU(z) of the tile that was asked for (zero past the end), and its B
+// and C, from the rows as they came.
+template <typename IO, typename SH>
+__device__ __forceinline__ void bwd_stage(const SelArgs& a, const SelPlace& p, int t0, int end, float* sm) {
+    using Raw = typename SH::template Raw<IO>;
+    const Raw& r = *reinterpret_cast<const Raw*>(sm + SH::O_RAW);
+    constexpr int PB = SH::PB, STEP = SH::THREADS / PB, NP = SH::NP;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < SH::L * NP; i += SH::THREADS) {
+        const int u = i / NP, n = i % NP;
+        const bool on = n < a.N;
+        sm[SH::O_BC + u * 2 * NP + n] = on ? to_f(r.B[u][n]) : 0.f;
+        sm[SH::O_BC + (u * 2 + 1) * NP + n] = on ? to_f(r.C[u][n]) : 0.f;
+    }
+    const int k = threadIdx.x % PB;
+    float2 bias = make_float2(0.f, 0.f);
+    if (a.dt_bias) {
+        if (2 * k < p.nc) bias.x = a.dt_bias[p.c0 + 2 * k];
+        if (2 * k + 1 < p.nc) bias.y = a.dt_bias[p.c0 + 2 * k + 1];
+    }
+#pragma unroll 2
+    for (int u = threadIdx.x / PB; u < SH::L; u += STEP) {
+        float2 delta = make_float2(0.f, 0.f), dx = delta, e = delta;
+        if (t0 + u < end) {
+            const float2 x = pair_of(&r.x[u][2 * k]), dt = pair_of(&r.dt[u][2 * k]);
+            e = pair_of(&r.dy[u][2 * k]);
+            if (a.z.p) {
+                const float2 z = pair_of(&r.z[u][2 * k]);
+                e.x *= z.x * sigmoid_f<IO>(z.x);
+                e.y *= z.y * sigmoid_f<IO>(z.y);
             }
+            delta.x = sel_delta(dt.x, bias.x, a.softplus);
+            delta.y = sel_delta(dt.y, bias.y, a.softplus);
+            dx.x = delta.x * x.x;
+            dx.y = delta.y * x.y;
         }
-#pragma unroll
-        for (int i = 0; i < U; i++) {
-            const int u = u0 + i * STEP;
-            float2 delta = make_float2(0.f, 0.f), dx = delta, e = delta;
-            if (t0 + u < end && one) {
-                const float2 xv = rx[i].f(), tv = rt[i].f();
-                e = ry[i].f();
-                if (a.z.p) {
-                    const float2 zv = rz[i].f();
-                    e.x *= zv.x * sigmoid_f<IO>(zv.x);
-                    e.y *= zv.y * sigmoid_f<IO>(zv.y);
-                }
-                delta.x = sel_delta(tv.x, bias.x, a.softplus);
-                delta.y = two ? sel_delta(tv.y, bias.y, a.softplus) : 0.f;
-                dx.x = delta.x * xv.x;
-                dx.y = delta.y * xv.y;
-            }
-            reinterpret_cast<float4*>(sm + SH::O_DD)[u * PB + k] = make_float4(delta.x, delta.y, dx.x, dx.y);
-            reinterpret_cast<float2*>(sm + SH::O_E)[u * PB + k] = e;
-        }
+        reinterpret_cast<float4*>(sm + SH::O_DD)[u * PB + k] = make_float4(delta.x, delta.y, dx.x, dx.y);
+        reinterpret_cast<float2*>(sm + SH::O_E)[u * PB + k] = e;
     }
 }
 
@@ -181,13 +202,16 @@ __global__ void __launch_bounds__(SH::THREADS, SH::LOCAL_BLOCKS) sel_bwd_local_k
         }
     }
     float total[2] = {0.f, 0.f};
+    if (p.t0 < end) bwd_request<IO, SH, WIDE>(a, p, p.t0, end, sm);
     for (int j = 0; j < tiles; j++) {
         const int t0 = p.t0 + j * L;
         const int count = min(L, end - t0);
         if (count > 0) {
+            cp_async_wait<0>();
+            __syncthreads();      // the rows are here; the tile before is done with
+            bwd_stage<IO, SH>(a, p, t0, end, sm);
             __syncthreads();
-            bwd_stage<IO, SH, WIDE>(a, p, t0, end, sm);
-            __syncthreads();
+            if (t0 + L < end && j + 1 < tiles) bwd_request<IO, SH, WIDE>(a, p, t0 + L, end, sm);
         }
 #pragma unroll 2
         for (int u = 0; u < count; u++) {
@@ -301,13 +325,12 @@ __global__ void __launch_bounds__(SH::THREADS, SH::MIN_BLOCKS) sel_bwd_kernel(co
     }
 
     const int tiles = a.seg / L;
-    for (int jt = tiles - 1; jt >= 0; jt--) {
+    const int last = end > p.t0 ? (end - p.t0 - 1) / L : -1;      // the last tile that holds tokens
+    if (last >= 0) bwd_request<IO, SH, WIDE>(a, p, p.t0 + last * L, end, sm);
+    for (int jt = last; jt >= 0; jt--) {
         const int t0 = p.t0 + jt * L;
         const int count = min(L, end - t0);
-        if (count <= 0) continue;
-        __syncthreads();
-        bwd_stage<IO, SH, WIDE>(a, p, t0, end, sm);
-        f2 h[2][NT / 2];
+        f2 h[2][NT / 2], h0[2][NT / 2];      // h0: the tile's entry state
 #pragma unroll
         for (int q = 0; q < 2; q++) {
             row_pairs<NT>(h[q], entry + row + q * a.N, q < mine, s * NT, a.N, 1.f);
@@ -321,20 +344,29 @@ __global__ void __launch_bounds__(SH::THREADS, SH::MIN_BLOCKS) sel_bwd_kernel(co
                 for (int i = 0; i < NT / 2; i++)
                     h[q][i] = fma2(ex2_2(mul2(pack2(sum, sum), A2[q][i])), h[q][i], own[i]);
             }
+#pragma unroll
+            for (int i = 0; i < NT / 2; i++) h0[q][i] = h[q][i];
         }
+        cp_async_wait<0>();
+        __syncthreads();      // the rows are here; the tile before is done with
+        bwd_stage<IO, SH>(a, p, t0, end, sm);
         __syncthreads();
+        if (jt > 0) bwd_request<IO, SH, WIDE>(a, p, t0 - L, end, sm);
 
         const float4* dd = reinterpret_cast<const float4*>(sm + SH::O_DD) + pl;
         const float2* ee = reinterpret_cast<const float2*>(sm + SH::O_E) + pl;
         const int pieces = (count + K - 1) / K;
-        // the state before each piece (a thread reads back its own values only)
+        // the state before each piece but the first and the last (a thread reads back its own
+        // values only)
+        auto kept = [&](int j, int q) {
+            return sm + SH::template O_CK<IO> + (((j - 1) * 2 + q) * PB + pl) * NP + s * NT;
+        };
         for (int j = 0; j < pieces; j++) {
+            if (j > 0 && j + 1 < pieces)
 #pragma unroll
-            for (int q = 0; q < 2; q++) {
-                f2* ck = reinterpret_cast<f2*>(sm + SH::O_CK + ((j * 2 + q) * PB + pl) * NP + s * NT);
+                for (int q = 0; q < 2; q++)
 #pragma unroll
-                for (int i = 0; i < NT / 2; i++) ck[i] = h[q][i];
-            }
+                    for (int i = 0; i < NT / 2; i++) reinterpret_cast<f2*>(kept(j, q))[i] = h[q][i];
             if (j + 1 < pieces) {
 #pragma unroll
                 for (int k = 0; k < K; k++) {
@@ -370,9 +402,17 @@ __global__ void __launch_bounds__(SH::THREADS, SH::MIN_BLOCKS) sel_bwd_kernel(co
                 }
             }
             f2 hp[K][2][NT / 2], dec[K][2][NT / 2];     // state before token k, decay of token k
+            if (j + 1 < pieces) {
+                if (j == 0) {
 #pragma unroll
-            for (int q = 0; q < 2; q++)
-                load_pairs(h[q], sm + SH::O_CK + ((j * 2 + q) * PB + pl) * NP + s * NT);
+                    for (int q = 0; q < 2; q++)
+#pragma unroll
+                        for (int i = 0; i < NT / 2; i++) h[q][i] = h0[q][i];
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 2; q++) load_pairs(h[q], kept(j, q));
+                }
+            }
 #pragma unroll
             for (int k = 0; k < K; k++) {
                 const int u = j * K + k;     // zero past the end: the state stays
@@ -431,7 +471,7 @@ __global__ void __launch_bounds__(SH::THREADS, SH::MIN_BLOCKS) sel_bwd_kernel(co
                 const int off = lane_sum<2 * NT, CW, 1>(over, lane);
                 constexpr int HOLD = 2 * NT > CW ? 2 * NT / CW : 1, SPARE = CW > 2 * NT ? CW / (2 * NT) : 1;
                 if (lane % SPARE == 0) {
-                    float* red = sm + SH::O_RED + (j & 1) * SH::RED + (wid * K + k) * 2 * NP;
+                    float* red = sm + SH::template O_RED<IO> + (j & 1) * SH::RED + (wid * K + k) * 2 * NP;
 #pragma unroll
                     for (int i = 0; i < HOLD; i++) {
                         const int v = off + i;
@@ -485,7 +525,7 @@ __global__ void __launch_bounds__(SH::THREADS, SH::MIN_BLOCKS) sel_bwd_kernel(co
             for (int i = threadIdx.x; i < K * 2 * NP; i += SH::THREADS) {
                 float v = 0.f;
 #pragma unroll
-                for (int w = 0; w < WARPS; w++) v += sm[SH::O_RED + (j & 1) * SH::RED + w * K * 2 * NP + i];
+                for (int w = 0; w < WARPS; w++) v += sm[SH::template O_RED<IO> + (j & 1) * SH::RED + w * K * 2 * NP + i];
                 const int t = t0 + j * K + i / (2 * NP);
                 if (t < end)
                     a.pBC[(((long long)p.b * a.T + t) * blks + blk) * 2 * NP + i % (2 * NP)] = v;
@@ -561,21 +601,22 @@ __global__ void __launch_bounds__(1024) sel_bwd_sum_kernel(const SelArgs a) {
 
 template <typename IO, typename SH, bool WIDE>
 cudaError_t bwd_w(const SelArgs& a, cudaStream_t s) {
+    static_assert(SH::template BYTES<IO> <= 227 * 1024, "");
     const int tiles = sel_tiles(a.D, a.G, SH::CB);
     const unsigned grid = (unsigned)((long long)tiles * a.nseg * a.batch);
-    cudaError_t e = allow_smem(sel_bwd_local_kernel<IO, SH, WIDE>, SH::LOCAL_BYTES);
-    if (e == cudaSuccess) e = allow_smem(sel_bwd_kernel<IO, SH, WIDE>, SH::BYTES);
+    cudaError_t e = allow_smem(sel_bwd_local_kernel<IO, SH, WIDE>, SH::template LOCAL_BYTES<IO>);
+    if (e == cudaSuccess) e = allow_smem(sel_bwd_kernel<IO, SH, WIDE>, SH::template BYTES<IO>);
     if (e != cudaSuccess) return e;
     const long long states = (long long)a.D * a.N;
     if (a.ntile > 1) {
-        sel_bwd_local_kernel<IO, SH, WIDE><<<grid, SH::THREADS, SH::LOCAL_BYTES, s>>>(a);
+        sel_bwd_local_kernel<IO, SH, WIDE><<<grid, SH::THREADS, SH::template LOCAL_BYTES<IO>, s>>>(a);
         const int blocks = (int)((states * a.batch + 127) / 128);
         sel_bwd_chain_kernel<<<2 * blocks, 128, 0, s>>>(a, blocks);
     }
-    sel_bwd_kernel<IO, SH, WIDE><<<grid, SH::THREADS, SH::BYTES, s>>>(a);
+    sel_bwd_kernel<IO, SH, WIDE><<<grid, SH::THREADS, SH::template BYTES<IO>, s>>>(a);
     const long long bc = (long long)a.batch * a.T * a.G * 2 * a.N;
     sel_bwd_bc_kernel<IO><<<(unsigned)((bc + 255) / 256), 256, 0, s>>>(a, SH::NP, tiles);
-    sel_bwd_sum_kernel<<<(unsigned)((states + 2 * a.D + 31) / 32), 1024, 0, s>>>(a);
+    sel_bwd_sum_kernel<<<(unsigned)((states + 2 * a.D + 31) / 32), column_threads(states + 2 * a.D), 0, s>>>(a);
     return cudaGetLastError();
 }
 

@@ -88,6 +88,13 @@ __device__ __forceinline__ void stage_rows(IO* sm, const View& v, int b, long lo
             const bool on = t0 + u < end && k < width;
             cp_async16(sm + u * W + k, on ? p + (t0 + u) * v.ts + k : p, on);
         }
+    } else if constexpr (sizeof(IO) == 4) {
+#pragma unroll 4
+        for (int i = threadIdx.x; i < L * W; i += THREADS) {
+            const int u = i / W, k = i % W;
+            const bool on = t0 + u < end && k < width;
+            cp_async4(sm + i, on ? p + (t0 + u) * v.ts + k : p, on);
+        }
     } else {
 #pragma unroll 8
         for (int i = threadIdx.x; i < L * W; i += THREADS) {
