@@ -64,6 +64,7 @@ void set_out(O& o, const m3_rows& r) {
 }
 
 constexpr int64_t kMaxBlocks = 2147483647;   // a one-dimensional grid
+constexpr int32_t kMaxTokens = 1 << 30;      // token numbers and a run more stay in 32 bits
 
 // ------------------------------------------------------------------ convolution
 
@@ -129,6 +130,7 @@ m3_status m3_conv_fwd(const m3_conv_dims* d, int32_t T, const m3_rows* x, const 
     m3_status st = conv_dims_ok(d);
     if (st != M3_OK) return st;
     if (T < 0) return M3_ERR_SHAPE;
+    if (T > kMaxTokens) return M3_ERR_UNSUPPORTED;
     if (flags & ~M3_FLAG_SILU) return M3_ERR_UNSUPPORTED;
     if (T == 0) return M3_OK;
     const Geo g{d->batch, T, esize(d->io_dtype), false};
@@ -166,6 +168,7 @@ m3_status m3_conv_bwd_workspace_bytes(const m3_conv_dims* d, int32_t T, size_t* 
     if (st != M3_OK) return st;
     if (!bytes) return M3_ERR_NULL;
     if (T < 0) return M3_ERR_SHAPE;
+    if (T > kMaxTokens) return M3_ERR_UNSUPPORTED;
     int seg, nseg;
     conv_runs(d, T, &seg, &nseg);
     const size_t n = sizeof(float) * (size_t)d->batch * nseg * (d->width + 1) * d->channels;
@@ -180,6 +183,7 @@ m3_status m3_conv_bwd(const m3_conv_dims* d, int32_t T, const m3_rows* x, const 
     m3_status st = conv_dims_ok(d);
     if (st != M3_OK) return st;
     if (T < 0) return M3_ERR_SHAPE;
+    if (T > kMaxTokens) return M3_ERR_UNSUPPORTED;
     if (flags & ~M3_FLAG_SILU) return M3_ERR_UNSUPPORTED;
     if (!gr || !gr->dweight || (bias && !gr->dbias)) return M3_ERR_NULL;
     if (!at_least(gr->dweight, 4) || (gr->dbias && !at_least(gr->dbias, 4)) ||
@@ -280,7 +284,7 @@ bool sel_grid_ok(const SelArgs& a) {
     const double cells = (double)a.batch * a.D * a.nseg;
     const double rows = (double)a.batch * a.T * a.G * 2 * a.N;
     return cells < 2147483647.0 && rows / 256 < 2147483646.0 &&
-           (double)a.batch * a.D * a.N / 128 < 2147483646.0;
+           (double)a.batch * a.D * a.N / 64 < 2147483646.0;
 }
 
 }  // namespace
@@ -292,6 +296,7 @@ m3_status m3_sel_workspace_bytes(const m3_sel_dims* d, int32_t T, size_t* bytes)
     if (st != M3_OK) return st;
     if (!bytes) return M3_ERR_NULL;
     if (T < 0) return M3_ERR_SHAPE;
+    if (T > kMaxTokens) return M3_ERR_UNSUPPORTED;
     const size_t n = T ? sel_fwd_workspace(d->batch, T, d->channels, d->ngroups, d->dstate) : 0;
     *bytes = n < 256 ? 256 : (n + 255) / 256 * 256;
     return M3_OK;
@@ -302,6 +307,7 @@ m3_status m3_sel_fwd(const m3_sel_dims* d, int32_t T, const m3_sel_inputs* in, f
     m3_status st = sel_dims_ok(d);
     if (st != M3_OK) return st;
     if (T < 0) return M3_ERR_SHAPE;
+    if (T > kMaxTokens) return M3_ERR_UNSUPPORTED;
     if (flags & ~M3_FLAG_DT_SOFTPLUS) return M3_ERR_UNSUPPORTED;
     if (ws && !at_least(ws, 256)) return M3_ERR_WORKSPACE;
     if (T == 0) return M3_OK;
@@ -351,6 +357,7 @@ m3_status m3_sel_bwd_workspace_bytes(const m3_sel_dims* d, int32_t T, size_t* by
     if (st != M3_OK) return st;
     if (!bytes) return M3_ERR_NULL;
     if (T < 0) return M3_ERR_SHAPE;
+    if (T > kMaxTokens) return M3_ERR_UNSUPPORTED;
     SelArgs a;
     std::memset(&a, 0, sizeof(a));
     a.batch = d->batch; a.T = T; a.D = d->channels; a.G = d->ngroups; a.N = d->dstate;
@@ -365,6 +372,7 @@ m3_status m3_sel_bwd(const m3_sel_dims* d, int32_t T, const m3_sel_inputs* in, c
     m3_status st = sel_dims_ok(d);
     if (st != M3_OK) return st;
     if (T < 0) return M3_ERR_SHAPE;
+    if (T > kMaxTokens) return M3_ERR_UNSUPPORTED;
     if (flags & ~M3_FLAG_DT_SOFTPLUS) return M3_ERR_UNSUPPORTED;
     if (!in || !gr || !gr->dA || (in->D && !gr->dD) || (in->dt_bias && !gr->ddt_bias))
         return M3_ERR_NULL;
