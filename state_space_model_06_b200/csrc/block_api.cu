@@ -76,16 +76,24 @@ m3_status conv_dims_ok(const m3_conv_dims* d) {
     return M3_OK;
 }
 
-// Tokens of a run: long enough that the W - 1 tokens read again at its start cost little (64: 5 %
-// from L2 at W 4), short enough that small calls still spread over the GPU.  At least 8, so that
-// only the first run reaches back into the state.
-void conv_runs(const m3_conv_dims* d, int32_t T, int* seg, int* nseg) {
-    const int64_t blocks = (int64_t)d->batch * ((d->channels + 511) / 512);
-    int s = 64;
-    while (s > 8 && blocks * ((T + s - 1) / s) < 148 * 4) s /= 2;
-    *seg = s;
-    *nseg = (T + s - 1) / s;
+// Tokens of a run.  A block's time is about its tokens and eight more (the filter, and the W - 1
+// tokens read again at its start), and `slots` blocks run at a time: of 8, 16, .. 128 tokens the
+// run that takes the least time in whole rounds of blocks.  At least 8, so that only the first run
+// reaches back into the state.
+void conv_runs(const m3_conv_dims* d, int32_t T, int slots, int* seg, int* nseg) {
+    const int64_t columns = (int64_t)d->batch * ((d->channels + 511) / 512);
+    int64_t best = 0;
+    for (int s = 8; s <= 128; s += 8) {
+        const int64_t n = ((int64_t)T + s - 1) / s;
+        const int64_t cost = (columns * n + slots - 1) / slots * (s + 8);
+        if (s == 8 || cost < best) {
+            best = cost;
+            *seg = s;
+            *nseg = (int)n;
+        }
+    }
 }
+constexpr int kConvFwdSlots = 148 * 7, kConvBwdSlots = 148 * 4;    // blocks an SM holds
 
 m3_status conv_common(const m3_conv_dims* d, const Geo& g, const m3_rows* x, const float* weight,
                       const float* bias, const int32_t* seqlens, const void* state, uint32_t flags) {
@@ -140,7 +148,7 @@ m3_status m3_conv_fwd(const m3_conv_dims* d, int32_t T, const m3_rows* x, const 
     ConvArgs a;
     conv_args(&a, d, T, x, weight, bias, seqlens, state, flags);
     set_out(a.y, *y);
-    conv_runs(d, T, &a.seg, &a.nseg);
+    conv_runs(d, T, kConvFwdSlots, &a.seg, &a.nseg);
     if ((int64_t)a.batch * a.nseg > kMaxBlocks) return M3_ERR_UNSUPPORTED;
     a.wide = conv_wide(d, weight, state) && wide_rows(*x, g) && wide_rows(*y, g);
     return status_of(launch_conv(a, ConvCall::fwd, d->io_dtype, static_cast<cudaStream_t>(stream)));
@@ -170,7 +178,7 @@ m3_status m3_conv_bwd_workspace_bytes(const m3_conv_dims* d, int32_t T, size_t* 
     if (T < 0) return M3_ERR_SHAPE;
     if (T > kMaxTokens) return M3_ERR_UNSUPPORTED;
     int seg, nseg;
-    conv_runs(d, T, &seg, &nseg);
+    conv_runs(d, T, kConvBwdSlots, &seg, &nseg);
     const size_t n = sizeof(float) * (size_t)d->batch * nseg * (d->width + 1) * d->channels;
     *bytes = n < 256 ? 256 : (n + 255) / 256 * 256;
     return M3_OK;
@@ -214,7 +222,7 @@ m3_status m3_conv_bwd(const m3_conv_dims* d, int32_t T, const m3_rows* x, const 
     a.dbias = bias ? gr->dbias : nullptr;
     a.dstate = gr->dstate;
     a.part = static_cast<float*>(ws);
-    conv_runs(d, T, &a.seg, &a.nseg);
+    conv_runs(d, T, kConvBwdSlots, &a.seg, &a.nseg);
     if ((int64_t)a.batch * a.nseg > kMaxBlocks) return M3_ERR_UNSUPPORTED;
     a.wide = conv_wide(d, weight, state0) && wide_rows(*x, g) && wide_rows(*dy, g) && wide_rows(gr->dx, g);
     return status_of(launch_conv(a, ConvCall::bwd, d->io_dtype, s));
