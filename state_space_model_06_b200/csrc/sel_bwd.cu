@@ -234,8 +234,10 @@ __global__ void __launch_bounds__(SH::THREADS, SH::LOCAL_BLOCKS) sel_bwd_local_k
                 }
             }
         }
-        if (t0 < p.t1) {      // a tile of the sequence (the last segment may have fewer)
-            const long long k = (long long)p.b * a.ntile + p.seg * tiles + j;
+        // at the end of each of the backward walk's tiles (the last segment may have fewer)
+        const int ends = (j + 1) * L;
+        if (ends % a.tile == 0 && p.t0 + ends - a.tile < p.t1) {
+            const long long k = (long long)p.b * a.ntile + p.seg * (a.seg / a.tile) + ends / a.tile - 1;
 #pragma unroll
             for (int q = 0; q < 2; q++) {
                 store_pairs<NT>(h[q], a.hloc + (k * a.D + c + q) * a.N, 2 * pl + q < p.nc, s * NT, a.N);
@@ -604,12 +606,15 @@ cudaError_t bwd_w(const SelArgs& a, cudaStream_t s) {
     static_assert(SH::template BYTES<IO> <= 227 * 1024, "");
     const int tiles = sel_tiles(a.D, a.G, SH::CB);
     const unsigned grid = (unsigned)((long long)tiles * a.nseg * a.batch);
-    cudaError_t e = allow_smem(sel_bwd_local_kernel<IO, SH, WIDE>, SH::template LOCAL_BYTES<IO>);
+    // the first step walks shorter tiles, so that more blocks fit an SM
+    using LSH = BwdShape<SH::NT, SH::S, SH::WARPS, 16, SH::K>;
+    static_assert(SH::L % LSH::L == 0, "");
+    cudaError_t e = allow_smem(sel_bwd_local_kernel<IO, LSH, WIDE>, LSH::template LOCAL_BYTES<IO>);
     if (e == cudaSuccess) e = allow_smem(sel_bwd_kernel<IO, SH, WIDE>, SH::template BYTES<IO>);
     if (e != cudaSuccess) return e;
     const long long states = (long long)a.D * a.N;
     if (a.ntile > 1) {
-        sel_bwd_local_kernel<IO, SH, WIDE><<<grid, SH::THREADS, SH::template LOCAL_BYTES<IO>, s>>>(a);
+        sel_bwd_local_kernel<IO, LSH, WIDE><<<grid, LSH::THREADS, LSH::template LOCAL_BYTES<IO>, s>>>(a);
         const int blocks = (int)((states * a.batch + 127) / 128);
         sel_bwd_chain_kernel<<<2 * blocks, 128, 0, s>>>(a, blocks);
     }

@@ -415,13 +415,16 @@ cudaError_t fwd_t(const SelArgs& a, cudaStream_t s) {
     return a.wide ? fwd_w<IO, SH, true>(a, s) : fwd_w<IO, SH, false>(a, s);
 }
 
-// The lane shape of a forward call, by the number of states.
+// The lane shape of a forward call, by the number of states.  For up to 16 states: with the whole
+// sequence in one piece the channels alone make the warps, so a lane holds two states (8 x 2048
+// tokens of 4096 channels: 494 us, 540 with four); segments bring as many warps as one likes, and
+// four states a lane take fewer instructions (16384 tokens of 2048 channels: 396 us, 436 with two).
 template <typename F>
-auto fwd_shape(int N, F f) {
+auto fwd_shape(int N, bool segments, F f) {
     if (N <= 4) return f(SelShape<2, 2, 2, 32>{});
     if (N <= 8) return f(SelShape<2, 4, 4, 32>{});
-    if (N <= 16) return f(SelShape<2, 8, 4, 32, 2>{});
-    if (N <= 32) return f(SelShape<4, 8, 4, 32>{});
+    if (N <= 16) return segments ? f(SelShape<4, 4, 4, 16>{}) : f(SelShape<2, 8, 4, 32, 2>{});
+    if (N <= 32) return f(SelShape<4, 8, 4, 16>{});
     if (N <= 64) return f(SelShape<8, 8, 4, 32>{});
     if (N <= 128) return f(SelShape<8, 16, 4, 32>{});
     return f(SelShape<16, 16, 4, 16>{});
@@ -463,21 +466,20 @@ cudaError_t step_t(const SelArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// Channels of a forward block.
-static int sel_fwd_channels(int N) {
-    return fwd_shape(N, [](auto sh) { return 2 * decltype(sh)::CB; });
-}
-
 // Segments.  A segmented call computes every decay twice (measured 1.75 times the work), so it
 // pays where the blocks of one pass would leave more than half of the GPU idle: then as many
-// segments as fill it once (seven blocks an SM), of at least two tiles of tokens.
+// segments as fill it about twice (14 blocks an SM: 378 us for 16384 tokens of 2048 channels, 397
+// with 8), of at least two tiles of tokens.
 int sel_fwd_segments(int batch, int T, int D, int G, int N, int* seg) {
+    auto blocks = [&](bool segments) {
+        const int CB = fwd_shape(N, segments, [](auto sh) { return 2 * decltype(sh)::CB; });
+        return (long long)batch * sel_tiles(D, G, CB);
+    };
     const int tiles = (T + kSelTile - 1) / kSelTile;
-    const long long blocks = (long long)batch * sel_tiles(D, G, sel_fwd_channels(N));
     int n = 1;
-    if (blocks <= 148 * 3) {
-        n = (int)(148 * 7 / blocks);
-        if (n > tiles / 2) n = tiles / 2;
+    if (blocks(false) <= 148 * 3) {
+        const long long want = 148 * 14 / blocks(true);
+        n = want > tiles / 2 ? tiles / 2 : (int)want;
         if (n < 1) n = 1;
     }
     const int per = (tiles + n - 1) / n;
@@ -492,7 +494,7 @@ size_t sel_fwd_workspace(int batch, int T, int D, int G, int N) {
 }
 
 cudaError_t launch_sel_fwd(const SelArgs& a, int io_dtype, cudaStream_t s) {
-    return fwd_shape(a.N, [&](auto sh) {
+    return fwd_shape(a.N, a.nseg > 1, [&](auto sh) {
         using SH = decltype(sh);
         return io_dtype == M3_BF16 ? fwd_t<__nv_bfloat16, SH>(a, s) : fwd_t<float, SH>(a, s);
     });
