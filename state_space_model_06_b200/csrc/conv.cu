@@ -1,8 +1,14 @@
 // conv.cu -- short causal convolution over the tokens, one filter a channel (m3_conv_*).
 //
-// y_t = act(bias + sum_k w[k] u_{t-W+1+k}).  A thread owns V neighbouring channels and walks a
+// y_t = act(bias + sum_k w[k] u_{t-W+1+k}).  A thread owns four neighbouring channels and walks a
 // run of tokens; the W - 1 tokens before the current one stay in registers, so every x is read
 // once from memory but for the W - 1 tokens at the start of a run.
+//
+// Memory bounds it.  Prompt, 8 x 4096 tokens of 4096 channels, W 4, SiLU: 94 us (5.7 TB/s; 82 us at
+// the copy rate); the first forms took 299 us (eight channels and scalar arithmetic: 120 registers,
+// 16 warps an SM) and 164 (packed pairs).  Backward, 4 x 2048 tokens: 58 us where the bytes would
+// take 31: 124 registers hold 16 warps an SM, and each token's chain (convolution, logistic, three
+// sums) is not covered by four warps a sub-partition; five blocks an SM spill (98 us).
 #include "block_internal.h"
 #include "block_common.cuh"
 

@@ -21,6 +21,14 @@
 // of states: the sums over channels (dB, dC) then cross half as many lanes, and they are what
 // would cost most (a value summed over 8 lanes takes 7/8 of a shuffle and four times that in
 // other instructions).
+//
+// Three passes over the exponentials (one in step 1, two in step 3) take 0.36 ms of the exponential
+// unit at 4 x 2048 tokens of 4096 channels of 16 states; it takes 1.18 ms in all (step 1 0.27, the
+// chain 0.03, step 3 0.87, the sums 0.03).  Step 3 is short of issue slots and of warps to fill
+// them: 528 instructions for 32 channel-tokens, of which a third is the walk itself, at 54 % of the
+// slots with 12 warps an SM (168 registers; at 128 the spills cost 40 %).  The first form (one channel
+// a lane, scalar arithmetic) took 1.99 ms; what brought most were the tokens' values asked for before
+// the piece that ends with them (0.38 ms) and the next tile's rows on their way during a tile (0.15).
 #include "block_internal.h"
 #include "sel_tile.cuh"
 
@@ -501,12 +509,21 @@ __global__ void __launch_bounds__(SH::THREADS, SH::MIN_BLOCKS) sel_bwd_kernel(co
                     if (a.z.p) {
                         const float2 z = rz[i].f(), dy = ry[i].f();
                         const float s0 = sigmoid_f<IO>(z.x), s1 = sigmoid_f<IO>(z.y);
-                        o[0] = dy.x * fmaf(skip[0], x.x, yv[0][i]) * fmaf(z.x * s0, 1.f - s0, s0);
-                        o[1] = dy.y * fmaf(skip[1], x.y, yv[1][i]) * fmaf(z.y * s1, 1.f - s1, s1);
+                        float y0 = yv[0][i], y1 = yv[1][i];
+                        if (a.Dskip) {      // no 0 * inf without D
+                            y0 = fmaf(skip[0], x.x, y0);
+                            y1 = fmaf(skip[1], x.y, y1);
+                        }
+                        o[0] = dy.x * y0 * fmaf(z.x * s0, 1.f - s0, s0);
+                        o[1] = dy.y * y1 * fmaf(z.y * s1, 1.f - s1, s1);
                         Vec<IO, 2>::template store<WIDE>(o, DZ.at(p.b, t) + c, mine);
                     }
-                    o[0] = fmaf(d.x, lb[0][i], skip[0] * e.x);
-                    o[1] = fmaf(d.y, lb[1][i], skip[1] * e.y);
+                    o[0] = d.x * lb[0][i];
+                    o[1] = d.y * lb[1][i];
+                    if (a.Dskip) {
+                        o[0] = fmaf(skip[0], e.x, o[0]);
+                        o[1] = fmaf(skip[1], e.y, o[1]);
+                    }
                     Vec<IO, 2>::template store<WIDE>(o, DX.at(p.b, t) + c, mine);
                     o[0] = fmaf(x.x, lb[0][i], la[0][i] * kLn2);
                     o[1] = fmaf(x.y, lb[1][i], la[1][i] * kLn2);

@@ -6,8 +6,16 @@
 //
 // Every (token, channel, state) needs an exponential, and every channel and state has a decay of
 // its own, so the chunked matrix form of the mixer's scan does not apply: the work is one ex2 and
-// four fp32 operations a cell on registers, and what bounds it is the exponential unit
-// (16 a clock and SM) well above the memory's share for N >= 8.
+// four fp32 operations a cell on registers.  The exponential unit (16 a clock and SM) bounds it:
+// 8 x 2048 tokens of 4096 channels of 16 states need 1.34e9 of them with softplus and gate, 298 us,
+// where the memory would take 83.  The prompt kernel takes 494 us there (the unit 58 % busy, issue
+// slots 68 %, shared memory 69 %): 185 instructions for 32 channel-tokens of 16 states, of which the
+// recurrence itself is half; the rest is the step and the gate (49), the sum over the lanes of a
+// channel (28) and the staging.  What was measured and not kept: two, four or eight tokens' decays
+// ahead of the chain through the states (no change), a quarter to a half of the exponentials by a
+// polynomial on the FMA pipe (3 to 16 % slower: issue slots are short too), one channel a lane
+// (650 us: the broadcast reads of B and C fill the shared memory), 8 and 16 states a lane (650 to
+// 800 us: too few warps).
 #include "block_internal.h"
 #include "sel_tile.cuh"
 
@@ -192,7 +200,11 @@ __global__ void __launch_bounds__(SH::THREADS) sel_scan_kernel(const SelArgs a) 
                 const int t = t0 + u;
                 if (mine && t < end) {
                     const float2 x = pair_of(&r.x[u][2 * pl]);
-                    float v[2] = {fmaf(skip[0], x.x, y[0]), fmaf(skip[1], x.y, y[1])};
+                    float v[2] = {y[0], y[1]};
+                    if (a.Dskip) {      // no 0 * inf without D
+                        v[0] = fmaf(skip[0], x.x, v[0]);
+                        v[1] = fmaf(skip[1], x.y, v[1]);
+                    }
                     if (a.z.p) {
                         const float2 z = pair_of(&r.z[u][2 * pl]);
                         v[0] *= z.x * sigmoid_f<IO>(z.x);
@@ -312,83 +324,72 @@ __global__ void __launch_bounds__(128) sel_step_kernel(const SelArgs a) {
 }
 
 // One token for N = 4 SL up to 32 and rows on 16 bytes: SL lanes share a channel, four states
-// each.  A warp takes 32 channels of ROWS sequences: each lane loads and prepares one channel's
-// x, dt and z; then SL turns go over 32 / SL channels each, whose states are one contiguous
-// stretch of memory.  A stays in registers over the sequences; the next sequence's states are on
-// their way while one is worked on.
-template <typename IO, int SL, int ROWS>
+// each.  A warp takes 32 channels of one sequence: each lane loads and prepares one channel's x, dt
+// and z; then SL turns go over 32 / SL channels each, whose states are one contiguous stretch of
+// memory.  The state's bytes bound it: 23.2 us at 256 sequences of 4096 channels of 16 states (6.2
+// TB/s).  Warps that keep A over 2, 4, 8 sequences take 30, 28, 28 us: they need twice the
+// registers, and half as many fit an SM.  Everything is asked for before anything is used: with D
+// loaded where it is needed, behind the sums, it takes 27 us.
+template <typename IO, int SL>
 __global__ void __launch_bounds__(128) sel_step_rows_kernel(const SelArgs a) {
     const int lane = threadIdx.x & 31, k = lane / SL, s = lane % SL;
     constexpr int CW = 32 / SL;                       // channels of a turn
     const int per_g = a.D / a.G, tiles_g = (per_g + 31) / 32;
-    const int tile = blockIdx.x * 4 + (threadIdx.x >> 5);
+    const int tile = blockIdx.x * 4 + (threadIdx.x >> 5), b = blockIdx.y;
     if (tile >= tiles_g * a.G) return;
     const int g = tile / tiles_g, c0 = g * per_g + (tile - g * tiles_g) * 32;
     const int nc = min(32, (g + 1) * per_g - c0);     // channels of this warp
-    const int b0 = blockIdx.y * ROWS, b1 = min(b0 + ROWS, a.batch);
     const int own = CW * s + k;                       // the channel this lane prepares and writes
     const bool mine = own < nc;
     const int c = c0 + (mine ? own : 0);
     const float bias = a.dt_bias ? a.dt_bias[c] : 0.f, skip = a.Dskip ? a.Dskip[c] : 0.f;
-    float4 A[SL], next[SL];
-    auto states = [&](int b, int i) {
-        return a.h + ((long long)b * a.D + c0 + i * CW + k) * (4 * SL) + 4 * s;
-    };
-    struct Token { IO x, dt, z; Quad4<IO> B, C; } tok;
-    auto request = [&](int b) {
+    float* state = a.h + ((long long)b * a.D + c0) * (4 * SL) + 4 * lane;
+    const float* rate = a.A + (long long)c0 * (4 * SL) + 4 * lane;
+    float4 h[SL], A[SL];
 #pragma unroll
-        for (int i = 0; i < SL; i++) {
-            next[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (i * CW + k < nc) next[i] = *reinterpret_cast<const float4*>(states(b, i));
-        }
-        tok.x = (static_cast<const IO*>(a.x.p) + b * a.x.bs)[c];
-        tok.dt = (static_cast<const IO*>(a.dt.p) + b * a.dt.bs)[c];
-        if (a.z.p) tok.z = (static_cast<const IO*>(a.z.p) + b * a.z.bs)[c];
-        const long long at = (long long)g * a.N + 4 * s;
-        tok.B = *reinterpret_cast<const Quad4<IO>*>(static_cast<const IO*>(a.B.p) + b * a.B.bs + at);
-        tok.C = *reinterpret_cast<const Quad4<IO>*>(static_cast<const IO*>(a.C.p) + b * a.C.bs + at);
-    };
-    request(b0);
+    for (int i = 0; i < SL; i++) {
+        h[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i * CW + k < nc) h[i] = *reinterpret_cast<const float4*>(state + i * 128);
+    }
+    const float x = to_f((static_cast<const IO*>(a.x.p) + b * a.x.bs)[c]);
+    const float dt = to_f((static_cast<const IO*>(a.dt.p) + b * a.dt.bs)[c]);
+    const float z = a.z.p ? to_f((static_cast<const IO*>(a.z.p) + b * a.z.bs)[c]) : 0.f;
+    const long long at = (long long)g * a.N + 4 * s;
+    const Quad4<IO> B4 = *reinterpret_cast<const Quad4<IO>*>(static_cast<const IO*>(a.B.p) + b * a.B.bs + at);
+    const Quad4<IO> C4 = *reinterpret_cast<const Quad4<IO>*>(static_cast<const IO*>(a.C.p) + b * a.C.bs + at);
 #pragma unroll
     for (int i = 0; i < SL; i++) {
         A[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (i * CW + k < nc) {
-            A[i] = *reinterpret_cast<const float4*>(a.A + (long long)(c0 + i * CW + k) * a.N + 4 * s);
+            A[i] = *reinterpret_cast<const float4*>(rate + i * 128);
             A[i].x *= kLog2e; A[i].y *= kLog2e; A[i].z *= kLog2e; A[i].w *= kLog2e;
         }
     }
-    for (int b = b0; b < b1; b++) {
-        const float x = to_f(tok.x), delta = sel_delta(to_f(tok.dt), bias, a.softplus), dx = delta * x;
-        const float z = a.z.p ? to_f(tok.z) : 0.f;
-        float Bv[4], Cv[4];
-        float4 h[SL];
+    float Bv[4], Cv[4];
 #pragma unroll
-        for (int j = 0; j < 4; j++) {
-            Bv[j] = to_f(tok.B.v[j]);
-            Cv[j] = to_f(tok.C.v[j]);
-        }
+    for (int j = 0; j < 4; j++) {
+        Bv[j] = to_f(B4.v[j]);
+        Cv[j] = to_f(C4.v[j]);
+    }
+    const float delta = sel_delta(dt, bias, a.softplus), dx = delta * x;
+    float y[SL];
 #pragma unroll
-        for (int i = 0; i < SL; i++) h[i] = next[i];
-        if (b + 1 < b1) request(b + 1);
-        float y[SL];
-#pragma unroll
-        for (int i = 0; i < SL; i++) {
-            // turn i works on channel i CW + k, which lane k SL + i of this warp prepared
-            const float d = __shfl_sync(0xffffffffu, delta, k * SL + i);
-            const float u = __shfl_sync(0xffffffffu, dx, k * SL + i);
-            h[i].x = fmaf(ex2(d * A[i].x), h[i].x, u * Bv[0]);
-            h[i].y = fmaf(ex2(d * A[i].y), h[i].y, u * Bv[1]);
-            h[i].z = fmaf(ex2(d * A[i].z), h[i].z, u * Bv[2]);
-            h[i].w = fmaf(ex2(d * A[i].w), h[i].w, u * Bv[3]);
-            y[i] = fmaf(Cv[0], h[i].x, fmaf(Cv[1], h[i].y, fmaf(Cv[2], h[i].z, Cv[3] * h[i].w)));
-            if (i * CW + k < nc) *reinterpret_cast<float4*>(states(b, i)) = h[i];
-        }
-        lane_sum<SL, SL, 1>(y, lane);      // lane k SL + i ends with channel i CW + k: its own
-        if (mine) {
-            float v = fmaf(skip, x, y[0]);
-            if (a.z.p) v *= z * sigmoid_f<IO>(z);
-            (static_cast<IO*>(a.y.p) + b * a.y.bs)[c] = from_f<IO>(v);
-        }
+    for (int i = 0; i < SL; i++) {
+        // turn i works on channel i CW + k, which lane k SL + i of this warp prepared
+        const float d = __shfl_sync(0xffffffffu, delta, k * SL + i);
+        const float u = __shfl_sync(0xffffffffu, dx, k * SL + i);
+        h[i].x = fmaf(ex2(d * A[i].x), h[i].x, u * Bv[0]);
+        h[i].y = fmaf(ex2(d * A[i].y), h[i].y, u * Bv[1]);
+        h[i].z = fmaf(ex2(d * A[i].z), h[i].z, u * Bv[2]);
+        h[i].w = fmaf(ex2(d * A[i].w), h[i].w, u * Bv[3]);
+        y[i] = fmaf(Cv[0], h[i].x, fmaf(Cv[1], h[i].y, fmaf(Cv[2], h[i].z, Cv[3] * h[i].w)));
+        if (i * CW + k < nc) *reinterpret_cast<float4*>(state + i * 128) = h[i];
+    }
+    lane_sum<SL, SL, 1>(y, lane);      // lane k SL + i ends with channel i CW + k: its own
+    if (mine) {
+        float v = a.Dskip ? fmaf(skip, x, y[0]) : y[0];      // no 0 * inf without D
+        if (a.z.p) v *= z * sigmoid_f<IO>(z);
+        (static_cast<IO*>(a.y.p) + b * a.y.bs)[c] = from_f<IO>(v);
     }
 }
 
@@ -432,14 +433,7 @@ auto fwd_shape(int N, bool segments, F f) {
 
 template <typename IO, int SL>
 cudaError_t step_rows_t(const SelArgs& a, cudaStream_t s) {
-    const int tiles = sel_tiles(a.D, a.G, 32);
-    const unsigned x = (unsigned)((tiles + 3) / 4);
-    // several sequences a warp where there are enough of them
-    if ((long long)tiles * a.batch >= 148 * 64) {
-        sel_step_rows_kernel<IO, SL, 4><<<dim3(x, (a.batch + 3) / 4), 128, 0, s>>>(a);
-    } else {
-        sel_step_rows_kernel<IO, SL, 1><<<dim3(x, a.batch), 128, 0, s>>>(a);
-    }
+    sel_step_rows_kernel<IO, SL><<<dim3((sel_tiles(a.D, a.G, 32) + 3) / 4, a.batch), 128, 0, s>>>(a);
     return cudaGetLastError();
 }
 
