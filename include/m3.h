@@ -421,8 +421,9 @@ m3_status m3_scan_bwd_ex(const m3_dims* dims, int32_t seqlen, const void* x, con
  * Conventions, beside those at the top of this file
  *   - Activations are m3_rows: [batch][T][width] tensors whose last axis is contiguous and
  *     whose batch and token strides are the caller's (a half of a projection's output, a
- *     transposed batch).  Input strides are >= 0 (0 reads one row again and again); output
- *     rows must not overlap one another (M3_ERR_SHAPE).  Outputs must not overlap inputs
+ *     transposed batch).  Input strides are >= 0 (0 reads one row again and again; its gradient
+ *     is still one row for each place, for the caller to add up); output rows must not overlap
+ *     one another (M3_ERR_SHAPE).  Outputs must not overlap inputs
  *     unless said so.  Any element alignment is accepted; rows that start on 16 bytes and are
  *     a multiple of 16 bytes long take the wide loads.
  *   - seqlens: device int32 [batch], or NULL for seqlen tokens in every sequence.  Sequence b

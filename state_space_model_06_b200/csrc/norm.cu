@@ -266,7 +266,7 @@ template <typename IO, typename RES, int OUT, bool WIDE>
 cudaError_t fwd_t(const NormArgs& a, cudaStream_t s) {
     auto go = [&](auto kernel, int tpr) {
         const int rpb = tpr < 128 ? 128 / tpr : 1;
-        kernel<<<(a.rows + rpb - 1) / rpb, tpr < 128 ? 128 : tpr, 0, s>>>(a);
+        kernel<<<(unsigned)(((long long)a.rows + rpb - 1) / rpb), tpr < 128 ? 128 : tpr, 0, s>>>(a);
         return cudaGetLastError();
     };
     switch (row_threads(a.d)) {

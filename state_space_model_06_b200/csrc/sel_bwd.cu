@@ -656,7 +656,7 @@ cudaError_t by_n(int N, F f) {
     if (N <= 32) return f(BwdShape<4, 8, 4, 32, 4>{});
     if (N <= 64) return f(BwdShape<4, 16, 4, 32, 4>{});
     if (N <= 128) return f(BwdShape<8, 16, 4, 16, 2>{});
-    return f(BwdShape<8, 32, 2, 32, 2>{});
+    return f(BwdShape<8, 32, 4, 16, 2>{});
 }
 
 }  // namespace

@@ -82,6 +82,7 @@ __device__ __forceinline__ void stage_rows(IO* sm, const View& v, int b, long lo
     const IO* p = static_cast<const IO*>(v.p) + b * v.bs + off;
     if constexpr (WIDE) {
         constexpr int V = 16 / sizeof(IO), PER = W / V;
+        static_assert(PER > 0 && W % V == 0, "a tile's rows are whole 16-byte pieces");
 #pragma unroll
         for (int i = threadIdx.x; i < L * PER; i += THREADS) {
             const int u = i / PER, k = (i % PER) * V;

@@ -150,6 +150,16 @@ def test_conv_bwd(case):
         near(gr[k], want[k], tol, k)
 
 
+@pytest.mark.parametrize("io", [BF, F32])
+@pytest.mark.parametrize("C", [64, 37])
+@pytest.mark.parametrize("W", range(1, 9))
+def test_conv_every_width(W, C, io):
+    """Each filter width, wide rows and narrow ones, forward and backward."""
+    case = (2, 45, C, W, io, "silu bias")
+    test_conv_fwd(case)
+    test_conv_bwd(case)
+
+
 # ---------------------------------------------------------------- selective scan
 
 SCAN = [  # b, T, ch, G, N, dtype, options
@@ -319,6 +329,40 @@ def test_scan_bwd(case):
         assert torch.equal(v, again[k]), k          # the same from run to run
 
 
+@pytest.mark.parametrize("io", [BF, F32])
+@pytest.mark.parametrize("ch", [48, 21])
+@pytest.mark.parametrize("N", [1, 3, 4, 5, 8, 12, 16, 20, 32, 40, 64, 72, 128, 200, 256])
+def test_scan_every_state_count(N, ch, io):
+    """Each lane shape, with wide rows and narrow ones: prompts (in one piece and in segments),
+    single tokens, backward over one tile and over several."""
+    opt = "z D bias softplus"
+    test_scan_fwd((1, 140, ch, 1, N, io, opt), True)
+    test_scan_fwd((1, 70, ch, 1, N, io, opt), False)
+    test_scan_step_continues_a_prompt((2, 5, ch, 1, N, io, opt))
+    test_scan_bwd((1, 70, ch, 1, N, io, opt))
+    test_scan_bwd((2, 9, ch, 1, N, io, opt))
+
+
+def test_scan_step_of_very_many_sequences():
+    """More sequences than a grid's second axis holds."""
+    test_scan_step_continues_a_prompt((66000, 1, 4, 1, 4, F32, "z D bias softplus"))
+
+
+def test_scan_without_skip_forms_no_nan():
+    """Without D an infinite x is not multiplied by zero: one state, so y is infinite."""
+    c, sl, sp = scan_inputs((1, 3, 8, 1, 1, F32, "softplus"), 18)
+    c["C"].fill_(1.0)
+    c["B"].fill_(1.0)
+    c["x"][0, 1] = float("inf")
+    y, _ = run_scan((1, 3, 8, 1, 1, F32, ""), c, sl, sp)
+    assert torch.isfinite(y[0, 0]).all() and (y[0, 1:] == float("inf")).all()
+    d = m3.SelDims(1, 8, 1, 1, m3.M3_F32)
+    ys = torch.empty(1, 8, device="cuda")
+    m3.m3_sel_step(d, c["x"][:, 1], c["dt"][:, 1], c["A"], c["B"][:, 1], c["C"][:, 1], None, None,
+                   None, c["h"], ys, flags=m3.M3_FLAG_DT_SOFTPLUS)
+    assert (ys == float("inf")).all()
+
+
 def test_scan_extreme_steps():
     """Decays that underflow, steps of zero, and softplus far out on both sides."""
     b, T, ch, N = 1, 40, 32, 16
@@ -465,6 +509,17 @@ def test_norm_bwd(case, inplace):
         near(dr, want, half_step(res) * want.abs() + tol, "dresidual")
     if w is not None:
         near(dw, want_w, (rows + rounds(d) + 16) * U32 * mag_w + 1e-37, "dweight")
+
+
+@pytest.mark.parametrize("io,res", [(BF, BF), (BF, F32), (F32, BF), (F32, F32), (BF, None)])
+@pytest.mark.parametrize("d", [8, 250, 256, 264, 512, 1000, 1024, 2048, 2056, 4096, 8192, 8200,
+                               16384, 16390, 24576, 32768])
+def test_norm_every_row_length(d, io, res):
+    """Each number of threads a row, wide rows and narrow ones."""
+    case = (5, d, io, res, "w")
+    test_norm_fwd(case, False)
+    test_norm_e4m3(case)
+    test_norm_bwd(case, False)
 
 
 def test_norm_non_finite_rows():
