@@ -460,10 +460,11 @@ cudaError_t step_t(const SelArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// Segments.  A segmented call computes every decay twice (measured 1.75 times the work), so it
-// pays where the blocks of one pass would leave more than half of the GPU idle: then as many
-// segments as fill it about twice (14 blocks an SM: 378 us for 16384 tokens of 2048 channels, 397
-// with 8), of at least two tiles of tokens.
+// Segments.  A segmented call computes every decay twice (measured 1.75 times the work) and takes
+// three launches instead of one, so it pays for more than about 128 tokens where the blocks of one
+// pass would leave more than half of the GPU idle: then as many segments as fill it about twice (14
+// blocks an SM: 378 us for 16384 tokens of 2048 channels, 397 with 8), down to one tile of tokens
+// each (3 x 509 tokens of 1001 channels: 37 us, 39 with two tiles at least).
 int sel_fwd_segments(int batch, int T, int D, int G, int N, int* seg) {
     auto blocks = [&](bool segments) {
         const int CB = fwd_shape(N, segments, [](auto sh) { return 2 * decltype(sh)::CB; });
@@ -471,9 +472,9 @@ int sel_fwd_segments(int batch, int T, int D, int G, int N, int* seg) {
     };
     const int tiles = (T + kSelTile - 1) / kSelTile;
     int n = 1;
-    if (blocks(false) <= 148 * 3) {
+    if (blocks(false) <= 148 * 3 && tiles > 4) {
         const long long want = 148 * 14 / blocks(true);
-        n = want > tiles / 2 ? tiles / 2 : (int)want;
+        n = want > tiles ? tiles : (int)want;
         if (n < 1) n = 1;
     }
     const int per = (tiles + n - 1) / n;

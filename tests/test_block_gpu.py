@@ -349,14 +349,14 @@ def test_scan_step_of_very_many_sequences():
 
 
 def test_scan_without_skip_forms_no_nan():
-    """Without D an infinite x is not multiplied by zero: one state, so y is infinite."""
-    c, sl, sp = scan_inputs((1, 3, 8, 1, 1, F32, "softplus"), 18)
+    """Without D an infinite x is not multiplied by zero: B and C are ones, so y is infinite."""
+    c, sl, sp = scan_inputs((1, 3, 8, 1, 4, F32, "softplus"), 18)
     c["C"].fill_(1.0)
     c["B"].fill_(1.0)
     c["x"][0, 1] = float("inf")
-    y, _ = run_scan((1, 3, 8, 1, 1, F32, ""), c, sl, sp)
+    y, _ = run_scan((1, 3, 8, 1, 4, F32, ""), c, sl, sp)
     assert torch.isfinite(y[0, 0]).all() and (y[0, 1:] == float("inf")).all()
-    d = m3.SelDims(1, 8, 1, 1, m3.M3_F32)
+    d = m3.SelDims(1, 8, 1, 4, m3.M3_F32)
     ys = torch.empty(1, 8, device="cuda")
     m3.m3_sel_step(d, c["x"][:, 1], c["dt"][:, 1], c["A"], c["B"][:, 1], c["C"][:, 1], None, None,
                    None, c["h"], ys, flags=m3.M3_FLAG_DT_SOFTPLUS)
