@@ -526,10 +526,9 @@ _PACK_CONV_DIMS = struct.Struct("4i").pack
 _PACK_SEL_DIMS = struct.Struct("5i").pack
 _PACK_NORM_DIMS = struct.Struct("5i").pack
 _PACK_ROWS = struct.Struct("Pqq").pack
-_PACK_CONV_GRADS = struct.Struct("PqqPPP").pack
-_PACK_SEL_INPUTS = struct.Struct("PqqPqqPqqPqqPqqPPPP").pack
-_PACK_SEL_GRADS = struct.Struct("PqqPqqPqqPqqPqqPPPP").pack
-_NO_ROWS = (0, 0, 0)
+_PACK_CONV_PARAMS = struct.Struct("PPP").pack      # behind dx: m3_conv_grads
+_PACK_POINTERS = struct.Struct("PPPP").pack        # behind five rows: m3_sel_inputs, m3_sel_grads
+_NO_ROWS = _PACK_ROWS(0, 0, 0)
 
 
 def _bad(status, name, t, what):
@@ -545,35 +544,45 @@ def _device(t, name):
     return dev
 
 
-def _rows(t, shape, lead, dtype, dev, name):
-    """An activation of this shape, whose axes after the first ``lead`` are contiguous, as the
-    fields of an m3_rows: address, batch stride, token stride."""
-    if t is None:
-        return _NO_ROWS
+def _must_be(t, shape, dtype, dev, name, contiguous):
+    """Raises what is wrong with a tensor (a last axis of one element may have any stride)."""
     if t.dtype is not dtype:
         _bad(M3_ERR_DTYPE, name, t, dtype)
     if t.shape != shape:
         _bad(M3_ERR_SHAPE, name, t, shape)
     if t.get_device() != dev:
         _bad(M3_ERR_UNSUPPORTED, name, t, f"device {dev}")
+    if not contiguous:
+        _bad(M3_ERR_SHAPE, name, t, "contiguous rows")
+
+
+def _rows(t, shape, dtype, dev, name):
+    """An activation of this shape ([batch, T, width] or [batch, width]) as a packed m3_rows."""
+    if t is None:
+        return _NO_ROWS
     st = t.stride()
-    if st[-1] != 1 and shape[-1] != 1:
-        _bad(M3_ERR_SHAPE, name, t, "a contiguous last axis")
-    if len(shape) > lead + 1 and st[lead] != shape[-1] and shape[lead] != 1:
-        _bad(M3_ERR_SHAPE, name, t, "contiguous groups")
-    return t.data_ptr(), st[0], st[1] if lead == 2 else 0
+    if st[-1] != 1 or t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _must_be(t, shape, dtype, dev, name, st[-1] == 1 or shape[-1] == 1)
+    return _PACK_ROWS(t.data_ptr(), st[0], st[1])
+
+
+def _group_rows(t, shape, dtype, dev, name):
+    """The same of B or C ([.., groups, states]): the groups of a row lie behind each other."""
+    if t is None:
+        return _NO_ROWS
+    st, n = t.stride(), shape[-1]
+    _must_be(t, shape, dtype, dev, name,
+             (st[-1] == 1 or n == 1) and (st[-2] == n or shape[-2] == 1))
+    return _PACK_ROWS(t.data_ptr(), st[0], st[1])
 
 
 def _packed(t, shape, dtype, dev, name):
     """A packed tensor's address (None: 0)."""
     if t is None:
         return 0
-    if t.dtype is not dtype:
-        _bad(M3_ERR_DTYPE, name, t, dtype)
-    if t.shape != shape or not t.is_contiguous():
-        _bad(M3_ERR_SHAPE, name, t, f"packed {shape}")
-    if t.get_device() != dev:
-        _bad(M3_ERR_UNSUPPORTED, name, t, f"device {dev}")
+    if (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()
+            or t.get_device() != dev):
+        _must_be(t, shape, dtype, dev, name, t.is_contiguous())
     return t.data_ptr()
 
 
@@ -581,13 +590,10 @@ def _matrix(t, shape, dtypes, dev, name):
     """A [rows, width] tensor's address and row stride."""
     if t is None:
         return 0, 0
-    if t.dtype not in dtypes:
-        _bad(M3_ERR_DTYPE, name, t, dtypes)
     st = t.stride()
-    if t.shape != shape or (st[1] != 1 and shape[1] != 1):
-        _bad(M3_ERR_SHAPE, name, t, shape)
-    if t.get_device() != dev:
-        _bad(M3_ERR_UNSUPPORTED, name, t, f"device {dev}")
+    if st[-1] != 1 or t.dtype not in dtypes or t.shape != shape or t.get_device() != dev:
+        _must_be(t, shape, t.dtype if t.dtype in dtypes else dtypes[0], dev, name,
+                 st[-1] == 1 or shape[-1] == 1)
     return t.data_ptr(), st[0]
 
 
@@ -605,16 +611,20 @@ def _run(name, dev, stream, *args):
     """Call the library on device ``dev``: on its current stream, or on ``stream``."""
     fn = getattr(_lib or load_library(), name)
     if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(dev)
+        stream = _raw_stream(dev)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if dev == torch._C._cuda_getDevice():
+    if dev == _current_device():
         status = fn(*args, stream)
     else:
         with torch.cuda.device(dev):
             status = fn(*args, stream)
-    if status != M3_OK:
+    if status:
         raise M3Error(status, name)
+
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _io_type(dims, name):
@@ -632,10 +642,9 @@ def m3_conv_fwd(dims: ConvDims, seqlen: int, x, weight, bias, state, y, seqlens=
     io, dev = _io_type(dims, name), _device(x, name)
     shape = (b, seqlen, C)
     _run(name, dev, stream, _PACK_CONV_DIMS(b, C, W, dims.io_dtype), seqlen,
-         _PACK_ROWS(*_rows(x, shape, 2, io, dev, name)), _packed(weight, (C, W), _F32, dev, name),
+         _rows(x, shape, io, dev, name), _packed(weight, (C, W), _F32, dev, name),
          _packed(bias, (C,), _F32, dev, name), _packed(seqlens, (b,), torch.int32, dev, name),
-         _packed(state, (b, W - 1, C), io, dev, name),
-         _PACK_ROWS(*_rows(y, shape, 2, io, dev, name)), flags)
+         _packed(state, (b, W - 1, C), io, dev, name), _rows(y, shape, io, dev, name), flags)
 
 
 def m3_conv_step(dims: ConvDims, x, weight, bias, state, y, flags: int = 0, stream=None):
@@ -644,9 +653,9 @@ def m3_conv_step(dims: ConvDims, x, weight, bias, state, y, flags: int = 0, stre
     io, dev = _io_type(dims, name), _device(x, name)
     shape = (b, C)
     _run(name, dev, stream, _PACK_CONV_DIMS(b, C, W, dims.io_dtype),
-         _PACK_ROWS(*_rows(x, shape, 1, io, dev, name)), _packed(weight, (C, W), _F32, dev, name),
+         _rows(x, shape, io, dev, name), _packed(weight, (C, W), _F32, dev, name),
          _packed(bias, (C,), _F32, dev, name), _packed(state, (b, W - 1, C), io, dev, name),
-         _PACK_ROWS(*_rows(y, shape, 1, io, dev, name)), flags)
+         _rows(y, shape, io, dev, name), flags)
 
 
 def m3_conv_bwd_workspace_bytes(dims: ConvDims, seqlen: int) -> int:
@@ -678,27 +687,27 @@ def m3_conv_bwd(dims: ConvDims, seqlen: int, x, weight, bias, state0, dy, grads:
     io, dev = _io_type(dims, name), _device(x, name)
     shape, get = (b, seqlen, C), grads.get
     _run(name, dev, stream, _PACK_CONV_DIMS(b, C, W, dims.io_dtype), seqlen,
-         _PACK_ROWS(*_rows(x, shape, 2, io, dev, name)), _packed(weight, (C, W), _F32, dev, name),
+         _rows(x, shape, io, dev, name), _packed(weight, (C, W), _F32, dev, name),
          _packed(bias, (C,), _F32, dev, name), _packed(seqlens, (b,), torch.int32, dev, name),
-         _packed(state0, (b, W - 1, C), io, dev, name),
-         _PACK_ROWS(*_rows(dy, shape, 2, io, dev, name)),
-         _PACK_CONV_GRADS(*_rows(get("dx"), shape, 2, io, dev, name),
-                          _packed(get("dweight"), (C, W), _F32, dev, name),
-                          _packed(get("dbias"), (C,), _F32, dev, name),
-                          _packed(get("dstate"), (b, W - 1, C), _F32, dev, name)),
+         _packed(state0, (b, W - 1, C), io, dev, name), _rows(dy, shape, io, dev, name),
+         _rows(get("dx"), shape, io, dev, name) + _PACK_CONV_PARAMS(
+             _packed(get("dweight"), (C, W), _F32, dev, name),
+             _packed(get("dbias"), (C,), _F32, dev, name),
+             _packed(get("dstate"), (b, W - 1, C), _F32, dev, name)),
          *_workspace(workspace, dev, name), flags)
 
 
 def _sel_inputs(dims, lead, x, dt, A, B, C, D, z, dt_bias, seqlens, dev, name):
     """The call's dims and m3_sel_inputs, packed; lead is (b, T) or (b,)."""
     io, b, ch, G, N = _io_type(dims, name), dims.batch, dims.channels, dims.ngroups, dims.dstate
-    k, wide, gn = len(lead), (*lead, ch), (*lead, G, N)
-    return _PACK_SEL_DIMS(b, ch, G, N, dims.io_dtype), _PACK_SEL_INPUTS(
-        *_rows(x, wide, k, io, dev, name), *_rows(dt, wide, k, io, dev, name),
-        *_rows(B, gn, k, io, dev, name), *_rows(C, gn, k, io, dev, name),
-        *_rows(z, wide, k, io, dev, name), _packed(A, (ch, N), _F32, dev, name),
-        _packed(D, (ch,), _F32, dev, name), _packed(dt_bias, (ch,), _F32, dev, name),
-        _packed(seqlens, (b,), torch.int32, dev, name))
+    wide, gn = (*lead, ch), (*lead, G, N)
+    return _PACK_SEL_DIMS(b, ch, G, N, dims.io_dtype), (
+        _rows(x, wide, io, dev, name) + _rows(dt, wide, io, dev, name)
+        + _group_rows(B, gn, io, dev, name) + _group_rows(C, gn, io, dev, name)
+        + _rows(z, wide, io, dev, name) + _PACK_POINTERS(
+            _packed(A, (ch, N), _F32, dev, name), _packed(D, (ch,), _F32, dev, name),
+            _packed(dt_bias, (ch,), _F32, dev, name),
+            _packed(seqlens, (b,), torch.int32, dev, name)))
 
 
 def m3_sel_workspace_bytes(dims: SelDims, seqlen: int) -> int:
@@ -722,7 +731,7 @@ def m3_sel_fwd(dims: SelDims, seqlen: int, x, dt, A, B, C, D, z, dt_bias, h, y, 
     packed = _sel_inputs(dims, lead, x, dt, A, B, C, D, z, dt_bias, seqlens, dev, name)
     _run(name, dev, stream, packed[0], seqlen, packed[1],
          _packed(h, (b, ch, dims.dstate), _F32, dev, name),
-         _PACK_ROWS(*_rows(y, (b, seqlen, ch), 2, _TYPE_OF[dims.io_dtype], dev, name)),
+         _rows(y, (b, seqlen, ch), _TYPE_OF[dims.io_dtype], dev, name),
          *_workspace(workspace, dev, name), flags)
 
 
@@ -732,7 +741,7 @@ def m3_sel_step(dims: SelDims, x, dt, A, B, C, D, z, dt_bias, h, y, flags: int =
     dev = _device(x, name)
     packed = _sel_inputs(dims, (b,), x, dt, A, B, C, D, z, dt_bias, None, dev, name)
     _run(name, dev, stream, *packed, _packed(h, (b, ch, dims.dstate), _F32, dev, name),
-         _PACK_ROWS(*_rows(y, (b, ch), 1, _TYPE_OF[dims.io_dtype], dev, name)), flags)
+         _rows(y, (b, ch), _TYPE_OF[dims.io_dtype], dev, name), flags)
 
 
 def m3_sel_bwd_workspace_bytes(dims: SelDims, seqlen: int) -> int:
@@ -770,12 +779,11 @@ def m3_sel_bwd(dims: SelDims, seqlen: int, x, dt, A, B, C, D, z, dt_bias, h0, dy
     packed = _sel_inputs(dims, lead, x, dt, A, B, C, D, z, dt_bias, seqlens, dev, name)
     io, wide, gn, hs = _TYPE_OF[dims.io_dtype], (b, seqlen, ch), (b, seqlen, G, N), (b, ch, N)
     _run(name, dev, stream, packed[0], seqlen, packed[1], _packed(h0, hs, _F32, dev, name),
-         _PACK_ROWS(*_rows(dy, wide, 2, io, dev, name)), _packed(dhT, hs, _F32, dev, name),
-         _PACK_SEL_GRADS(
-             *_rows(get("dx"), wide, 2, io, dev, name), *_rows(get("ddt"), wide, 2, io, dev, name),
-             *_rows(get("dB"), gn, 2, io, dev, name), *_rows(get("dC"), gn, 2, io, dev, name),
-             *_rows(get("dz"), wide, 2, io, dev, name), _packed(get("dA"), (ch, N), _F32, dev, name),
-             _packed(get("dD"), (ch,), _F32, dev, name),
+         _rows(dy, wide, io, dev, name), _packed(dhT, hs, _F32, dev, name),
+         _rows(get("dx"), wide, io, dev, name) + _rows(get("ddt"), wide, io, dev, name)
+         + _group_rows(get("dB"), gn, io, dev, name) + _group_rows(get("dC"), gn, io, dev, name)
+         + _rows(get("dz"), wide, io, dev, name) + _PACK_POINTERS(
+             _packed(get("dA"), (ch, N), _F32, dev, name), _packed(get("dD"), (ch,), _F32, dev, name),
              _packed(get("ddt_bias"), (ch,), _F32, dev, name),
              _packed(get("dh"), hs, _F32, dev, name)),
          *_workspace(workspace, dev, name), flags)

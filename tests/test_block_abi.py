@@ -27,15 +27,18 @@ def rows(ptr=P, bs=64 * 16, ts=16):
 
 
 def test_packed_layouts_match_the_header(tmp_path):
-    structs = dict(m3_rows=(m3.m3_rows, "PACK_ROWS"), m3_conv_dims=(m3.m3_conv_dims, "PACK_CONV_DIMS"),
-                   m3_conv_grads=(m3.m3_conv_grads, "PACK_CONV_GRADS"),
-                   m3_sel_dims=(m3.m3_sel_dims, "PACK_SEL_DIMS"),
-                   m3_sel_inputs=(m3.m3_sel_inputs, "PACK_SEL_INPUTS"),
-                   m3_sel_grads=(m3.m3_sel_grads, "PACK_SEL_GRADS"),
-                   m3_norm_dims=(m3.m3_norm_dims, "PACK_NORM_DIMS"))
+    """What the binding packs has the sizes and offsets of the C structs."""
+    rows = m3._PACK_ROWS.__self__.size
+    packs = dict(m3_rows=rows, m3_conv_dims=m3._PACK_CONV_DIMS.__self__.size,
+                 m3_conv_grads=rows + m3._PACK_CONV_PARAMS.__self__.size,
+                 m3_sel_dims=m3._PACK_SEL_DIMS.__self__.size,
+                 m3_sel_inputs=5 * rows + m3._PACK_POINTERS.__self__.size,
+                 m3_sel_grads=5 * rows + m3._PACK_POINTERS.__self__.size,
+                 m3_norm_dims=m3._PACK_NORM_DIMS.__self__.size)
     src = tmp_path / "layout.c"
     lines = []
-    for name, (ct, _) in structs.items():
+    for name in packs:
+        ct = getattr(m3, name)
         lines.append('printf("%%zu", sizeof(%s));' % name)
         lines += ['printf(" %%zu", offsetof(%s, %s));' % (name, f[0]) for f in ct._fields_]
         lines.append('printf("\\n");')
@@ -44,10 +47,11 @@ def test_packed_layouts_match_the_header(tmp_path):
     exe = tmp_path / "layout"
     subprocess.check_call(["gcc", "-I", os.path.join(ROOT, "include"), "-o", str(exe), str(src)])
     out = subprocess.check_output([str(exe)]).decode().splitlines()
-    for line, (name, (ct, pack)) in zip(out, structs.items()):
+    for line, (name, size) in zip(out, packs.items()):
+        ct = getattr(m3, name)
         want = [int(v) for v in line.split()]
         assert want == [ctypes.sizeof(ct)] + [getattr(ct, f[0]).offset for f in ct._fields_], name
-        assert getattr(m3, "_" + pack).__self__.size == ctypes.sizeof(ct), name
+        assert size == want[0], name
 
 
 # ---------------------------------------------------------------- convolution
