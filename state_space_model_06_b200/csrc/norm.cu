@@ -80,7 +80,16 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_fwd_kernel(const N
         for (int j = 0; j < 8; j++) ss[0] = fmaf(r[v][j], r[v][j], ss[0]);
     }
     row_sum<TPR>(ss, sm);
-    const float rstd = 1.f / sqrtf(ss[0] / (float)a.d + a.eps);
+    const float mean = ss[0] / (float)a.d + a.eps, rstd = 1.f / sqrtf(mean);
+    // In e4m3 an error of one ulp of y that crosses the middle of two steps costs a whole step, so
+    // y = r / sqrt(mean) is formed with the reciprocal root's remainder: rstd + low is it to twice
+    // the digits (one Newton step on mean rstd^2 = 1, the products' low parts by FMA).
+    float low = 0.f;
+    if constexpr (OUT == M3_OUT_E4M3) {
+        const float p = mean * rstd, e = fmaf(mean, rstd, -p);
+        low = 0.5f * rstd * (fmaf(-p, rstd, 1.f) - e * rstd);
+        if (!(fabsf(low) < rstd)) low = 0.f;      // a mean of 0, infinity or NaN has no remainder
+    }
 #pragma unroll
     for (int v = 0; v < NV; v++) {
         const int i = (k + v * TPR) * 8, n = live ? min(max(a.d - i, 0), 8) : 0;
@@ -91,6 +100,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_fwd_kernel(const N
 #pragma unroll
         for (int j = 0; j < 8; j++) {
             y[j] = r[v][j] * rstd;
+            if constexpr (OUT == M3_OUT_E4M3) y[j] += fmaf(r[v][j], low, fmaf(r[v][j], rstd, -y[j]));
             if (a.weight) y[j] *= w[j];
         }
         if constexpr (OUT == M3_OUT_IO) {
