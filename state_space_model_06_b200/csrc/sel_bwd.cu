@@ -37,14 +37,11 @@ namespace m3 {
 namespace {
 
 template <int NT_, int S_, int WARPS_, int L_, int K_>
-struct BwdShape {
-    static constexpr int NT = NT_, S = S_, WARPS = WARPS_;
-    static constexpr int L = L_, K = K_;         // tokens of a tile, of a piece
-    static constexpr int CW = 32 / S;            // pairs of channels of a warp
-    static constexpr int PB = CW * WARPS;        // pairs of channels of a block
-    static constexpr int CB = 2 * PB;            // channels of a block
-    static constexpr int NP = NT * S;            // states, padded
-    static constexpr int THREADS = 32 * WARPS;
+struct BwdShape : SelShape<NT_, S_, WARPS_, L_> {
+    using Base = SelShape<NT_, S_, WARPS_, L_>;
+    using Base::NT; using Base::WARPS; using Base::L; using Base::PB; using Base::CB;
+    using Base::NP; using Base::THREADS;
+    static constexpr int K = K_;                 // tokens of a piece
     static constexpr int MIN_BLOCKS = NT * K <= 16 ? 384 / THREADS : 1;   // 168 registers a thread
     static constexpr int LOCAL_BLOCKS = NT == 4 ? 640 / THREADS : 1;      // 102 registers
     // shared memory, in floats
@@ -67,7 +64,6 @@ struct BwdShape {
     static constexpr int LOCAL_BYTES = 4 * O_CK<IO>;
     template <typename IO>
     static constexpr int BYTES = 4 * (O_RED<IO> + 2 * RED);
-    static_assert(THREADS % PB == 0, "");
 };
 
 // Two neighbouring values of a row, as they are (`two` false: the second is not there).

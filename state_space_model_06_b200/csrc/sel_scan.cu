@@ -37,7 +37,7 @@ namespace {
 // busy.  Two channels a lane halve the reads of B and C; four states a lane leave enough warps.
 template <typename IO, typename SH>
 struct FwdSmem {
-    static constexpr int L = SH::L, CB = SH::CB * 2;
+    static constexpr int L = SH::L, CB = SH::CB;
     // B and C rows keep a multiple of 16 bytes
     static constexpr int NR = (SH::NP * (int)sizeof(IO) + 15) / 16 * 16 / (int)sizeof(IO);
     struct Raw {
@@ -50,8 +50,9 @@ struct FwdSmem {
 
 template <typename IO, typename SH, bool WIDE, bool LOCAL>
 __global__ void __launch_bounds__(SH::THREADS) sel_scan_kernel(const SelArgs a) {
-    constexpr int L = SH::L, NT = SH::NT, S = SH::S, CW = SH::CW, CB = SH::CB * 2, NP = SH::NP;
+    constexpr int L = SH::L, NT = SH::NT, S = SH::S, CW = SH::CW, CB = SH::CB, NP = SH::NP;
     constexpr int THREADS = SH::THREADS;
+    static_assert(L % S == 0, "");
     using Smem = FwdSmem<IO, SH>;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
@@ -108,7 +109,6 @@ __global__ void __launch_bounds__(SH::THREADS) sel_scan_kernel(const SelArgs a) 
         for (int q = 0; q < 2; q++)
             if (q < mine) skip[q] = a.Dskip[c + q];
     // the pair of channels whose deltas this thread lays out
-    static_assert(THREADS % (CB / 2) == 0, "");
     const int kd = threadIdx.x % (CB / 2);
     float bias[2] = {0.f, 0.f};
     if (a.dt_bias)
@@ -146,51 +146,32 @@ __global__ void __launch_bounds__(SH::THREADS) sel_scan_kernel(const SelArgs a) 
         __syncthreads();
         const int count = min(L, end - t0);
         for (int u0 = 0; u0 < count; u0 += S) {
-            // G tokens at a time: first what depends on no state (the decays and the inputs),
-            // then the chain through the states, so that the exponentials of several tokens
-            // are in flight together
-            constexpr int G = SH::GT < S ? SH::GT : S;
             float y[2 * S];
 #pragma unroll
-            for (int g0 = 0; g0 < S; g0 += G) {
-                f2 dec[G][2][NT / 2], in[G][2][NT / 2];
+            for (int u = 0; u < S; u++) {
+                const float4 d = sm.dd[u0 + u][pl];       // zero past the end: h stays
+                const f2 delta[2] = {pack2(d.x, d.x), pack2(d.y, d.y)};
+                const f2 dx[2] = {pack2(d.z, d.z), pack2(d.w, d.w)};
+                f2 B[NT / 2], C[NT / 2], acc[2];
+                load_pairs(B, &sm.bc[u0 + u][0][s * NT]);
+                if (!LOCAL) load_pairs(C, &sm.bc[u0 + u][1][s * NT]);
 #pragma unroll
-                for (int g = 0; g < G; g++) {
-                    const int u = u0 + g0 + g;
-                    const float4 d = sm.dd[u][pl];       // zero past the end: h stays
-                    f2 B[NT / 2];
-                    load_pairs(B, &sm.bc[u][0][s * NT]);
+                for (int i = 0; i < NT / 2; i++)
 #pragma unroll
-                    for (int i = 0; i < NT / 2; i++) {
-                        dec[g][0][i] = ex2_2(mul2(pack2(d.x, d.x), A2[0][i]));
-                        dec[g][1][i] = ex2_2(mul2(pack2(d.y, d.y), A2[1][i]));
-                        in[g][0][i] = mul2(pack2(d.z, d.z), B[i]);
-                        in[g][1][i] = mul2(pack2(d.w, d.w), B[i]);
+                    for (int q = 0; q < 2; q++) {
+                        h[q][i] = fma2(ex2_2(mul2(delta[q], A2[q][i])), h[q][i], mul2(dx[q], B[i]));
+                        if (!LOCAL)
+                            acc[q] = i == 0 ? mul2(C[i], h[q][i]) : fma2(C[i], h[q][i], acc[q]);
                     }
-                    if (LOCAL) {
-                        total[0] += d.x;
-                        total[1] += d.y;
-                    }
-                }
+                if (LOCAL) {
+                    total[0] += d.x;
+                    total[1] += d.y;
+                } else {
 #pragma unroll
-                for (int g = 0; g < G; g++) {
-                    f2 C[NT / 2], acc[2];
-                    if (!LOCAL) load_pairs(C, &sm.bc[u0 + g0 + g][1][s * NT]);
-#pragma unroll
-                    for (int i = 0; i < NT / 2; i++)
-#pragma unroll
-                        for (int q = 0; q < 2; q++) {
-                            h[q][i] = fma2(dec[g][q][i], h[q][i], in[g][q][i]);
-                            if (!LOCAL)
-                                acc[q] = i == 0 ? mul2(C[i], h[q][i]) : fma2(C[i], h[q][i], acc[q]);
-                        }
-                    if (!LOCAL) {
-#pragma unroll
-                        for (int q = 0; q < 2; q++) {
-                            float lo, hi;
-                            unpack2(acc[q], lo, hi);
-                            y[2 * (g0 + g) + q] = lo + hi;
-                        }
+                    for (int q = 0; q < 2; q++) {
+                        float lo, hi;
+                        unpack2(acc[q], lo, hi);
+                        y[2 * u + q] = lo + hi;
                     }
                 }
             }
@@ -397,7 +378,7 @@ template <typename IO, typename SH, bool WIDE>
 cudaError_t fwd_w(const SelArgs& a, cudaStream_t s) {
     constexpr int bytes = (int)sizeof(FwdSmem<IO, SH>);
     static_assert(bytes <= 227 * 1024, "");
-    const unsigned grid = (unsigned)((long long)sel_tiles(a.D, a.G, 2 * SH::CB) * a.nseg * a.batch);
+    const unsigned grid = (unsigned)((long long)sel_tiles(a.D, a.G, SH::CB) * a.nseg * a.batch);
     cudaError_t e = allow_smem(sel_scan_kernel<IO, SH, WIDE, false>, bytes);
     if (e != cudaSuccess) return e;
     if (a.nseg > 1) {
@@ -424,7 +405,7 @@ template <typename F>
 auto fwd_shape(int N, bool segments, F f) {
     if (N <= 4) return f(SelShape<2, 2, 2, 32>{});
     if (N <= 8) return f(SelShape<2, 4, 4, 32>{});
-    if (N <= 16) return segments ? f(SelShape<4, 4, 4, 16>{}) : f(SelShape<2, 8, 4, 32, 2>{});
+    if (N <= 16) return segments ? f(SelShape<4, 4, 4, 16>{}) : f(SelShape<2, 8, 4, 32>{});
     if (N <= 32) return f(SelShape<4, 8, 4, 16>{});
     if (N <= 64) return f(SelShape<8, 8, 4, 32>{});
     if (N <= 128) return f(SelShape<8, 16, 4, 32>{});
@@ -467,7 +448,7 @@ cudaError_t step_t(const SelArgs& a, cudaStream_t s) {
 // each (3 x 509 tokens of 1001 channels: 37 us, 39 with two tiles at least).
 int sel_fwd_segments(int batch, int T, int D, int G, int N, int* seg) {
     auto blocks = [&](bool segments) {
-        const int CB = fwd_shape(N, segments, [](auto sh) { return 2 * decltype(sh)::CB; });
+        const int CB = fwd_shape(N, segments, [](auto sh) { return decltype(sh)::CB; });
         return (long long)batch * sel_tiles(D, G, CB);
     };
     const int tiles = (T + kSelTile - 1) / kSelTile;

@@ -1,23 +1,25 @@
 // sel_tile.cuh -- how the selective scan's kernels lay a tile out over lanes and shared memory.
 //
-// A channel's N states are spread over S lanes (a power of two), NT states each, so a warp
-// holds 32 / S channels.  Lane l of a warp owns channel l % CW and states (l / CW) NT ..: lanes
-// that differ in the high bits share a channel, neighbouring lanes hold neighbouring channels.
+// A channel's N states are spread over S lanes (a power of two), NT states each, and a lane holds
+// two neighbouring channels, so a warp holds CW = 32 / S pairs of channels.  Lane l of a warp owns
+// pair l % CW and states (l / CW) NT ..: lanes that differ in the high bits share a pair,
+// neighbouring lanes hold neighbouring pairs.
 #pragma once
 
 #include "block_common.cuh"
 
 namespace m3 {
 
-template <int NT_, int S_, int WARPS_, int L_ = kSelTile, int GT_ = 1>
+template <int NT_, int S_, int WARPS_, int L_>
 struct SelShape {
-    static constexpr int GT = GT_;               // tokens whose decays are computed together
     static constexpr int NT = NT_, S = S_, WARPS = WARPS_;
-    static constexpr int L = L_;                 // tokens staged together (S divides it)
-    static constexpr int CW = 32 / S;            // channels of a warp
-    static constexpr int CB = CW * WARPS;        // channels of a block
+    static constexpr int L = L_;                 // tokens of a tile
+    static constexpr int CW = 32 / S;            // pairs of channels of a warp
+    static constexpr int PB = CW * WARPS;        // pairs of channels of a block
+    static constexpr int CB = 2 * PB;            // channels of a block
     static constexpr int NP = NT * S;            // states, padded
     static constexpr int THREADS = 32 * WARPS;
+    static_assert(THREADS % PB == 0, "");
 };
 
 // Where a block works: its batch row, segment and channels.  A block's channels all lie in one
@@ -114,23 +116,6 @@ __device__ __forceinline__ float2 pair_of(const IO* p) {
         return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(p));
     } else {
         return *reinterpret_cast<const float2*>(p);
-    }
-}
-
-// B and C of tokens t0 .. t0 + L - 1 as floats in sm[L][2][NP]; tokens at or past `end` and
-// states past N read zero.
-template <typename IO, int NP, int L, int THREADS>
-__device__ __forceinline__ void sel_stage_bc(const SelArgs& a, const SelPlace& p, int t0, int end,
-                                             float* sm) {
-    const IO* pb = static_cast<const IO*>(a.B.p) + p.b * a.B.bs + (long long)p.g * a.N;
-    const IO* pc = static_cast<const IO*>(a.C.p) + p.b * a.C.bs + (long long)p.g * a.N;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < L * 2 * NP; i += THREADS) {
-        const int n = i % NP, which = (i / NP) & 1, t = t0 + i / (2 * NP);
-        float v = 0.f;
-        if (t < end && n < a.N)
-            v = to_f(which ? pc[t * a.C.ts + n] : pb[t * a.B.ts + n]);
-        sm[i] = v;
     }
 }
 
