@@ -8,7 +8,8 @@
 // the copy rate); the first forms took 299 us (eight channels and scalar arithmetic: 120 registers,
 // 16 warps an SM) and 164 (packed pairs).  Backward, 4 x 2048 tokens: 58 us where the bytes would
 // take 31: 124 registers hold 16 warps an SM, and each token's chain (convolution, logistic, three
-// sums) is not covered by four warps a sub-partition; five blocks an SM spill (98 us).
+// sums) is not covered by four warps a sub-partition; five blocks an SM spill (98 us), and two
+// channels a thread, with 28 warps, double the copies and addresses (62 us).
 #include "block_internal.h"
 #include "block_common.cuh"
 
