@@ -25,8 +25,9 @@
 // Three passes over the exponentials (one in step 1, two in step 3) take 0.36 ms of the exponential
 // unit at 4 x 2048 tokens of 4096 channels of 16 states; it takes 1.18 ms in all (step 1 0.27, the
 // chain 0.03, step 3 0.87, the sums 0.03).  Step 3 is short of issue slots and of warps to fill
-// them: 528 instructions for 32 channel-tokens, of which a third is the walk itself, at 54 % of the
-// slots with 12 warps an SM (168 registers; at 128 the spills cost 40 %).  The first form (one channel
+// them: 532 instructions for 32 channel-tokens, of which a third is the walk itself, at 54 % of the
+// slots with 12 warps an SM (168 registers; at 128 the spills cost 40 %, and
+// decays recomputed instead of kept bring 16 warps and nothing: the instructions grow as much).  The first form (one channel
 // a lane, scalar arithmetic) took 1.99 ms; what brought most were the tokens' values asked for before
 // the piece that ends with them (0.38 ms) and the next tile's rows on their way during a tile (0.15).
 #include "block_internal.h"

@@ -8,8 +8,8 @@
 // its own, so the chunked matrix form of the mixer's scan does not apply: the work is one ex2 and
 // four fp32 operations a cell on registers.  The exponential unit (16 a clock and SM) bounds it:
 // 8 x 2048 tokens of 4096 channels of 16 states need 1.34e9 of them with softplus and gate, 298 us,
-// where the memory would take 83.  The prompt kernel takes 494 us there (the unit 58 % busy, issue
-// slots 68 %, shared memory 69 %): 185 instructions for 32 channel-tokens of 16 states, of which the
+// where the memory would take 83.  The prompt kernel takes 500 us there (the unit 58 % busy, issue
+// slots 68 %, shared memory 69 %): 189 instructions for 32 channel-tokens of 16 states, of which the
 // recurrence itself is half; the rest is the step and the gate (49), the sum over the lanes of a
 // channel (28) and the staging.  What was measured and not kept: two, four or eight tokens' decays
 // ahead of the chain through the states (no change), a quarter to a half of the exponentials by a
