@@ -454,7 +454,8 @@ typedef struct {
  *           NULL; both 4-byte aligned
  *   state   [batch][W-1][channels] io dtype, packed, oldest token first, updated in place
  *           (zeros start a sequence).  NULL is allowed for W = 1 alone.
- * Width W is 1 to 8.  Flags: M3_FLAG_SILU.  seqlen 0 does nothing.
+ * Width W is 1 to 8.  Flags: M3_FLAG_SILU.  seqlen 0 does nothing.  y may not be x, nor dx x or
+ * dy (M3_ERR_UNSUPPORTED): tokens are read for their neighbours too.
  */
 typedef struct {
     int32_t batch;

@@ -145,6 +145,7 @@ m3_status m3_conv_fwd(const m3_conv_dims* d, int32_t T, const m3_rows* x, const 
     if ((st = conv_common(d, g, x, weight, bias, seqlens, state, flags)) != M3_OK) return st;
     if (!y) return M3_ERR_NULL;
     if ((st = check_out(*y, g, d->channels)) != M3_OK) return st;
+    if (y->ptr == x->ptr) return M3_ERR_UNSUPPORTED;      // a run reads tokens of the one before
     ConvArgs a;
     conv_args(&a, d, T, x, weight, bias, seqlens, state, flags);
     set_out(a.y, *y);
@@ -211,6 +212,7 @@ m3_status m3_conv_bwd(const m3_conv_dims* d, int32_t T, const m3_rows* x, const 
     if (!dy) return M3_ERR_NULL;
     if ((st = check_in(*dy, g)) != M3_OK) return st;
     if ((st = check_out(gr->dx, g, d->channels)) != M3_OK) return st;
+    if (gr->dx.ptr == x->ptr || gr->dx.ptr == dy->ptr) return M3_ERR_UNSUPPORTED;
     size_t need;
     m3_conv_bwd_workspace_bytes(d, T, &need);
     if (!ws || !at_least(ws, 256) || ws_bytes < need) return M3_ERR_WORKSPACE;

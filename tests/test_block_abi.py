@@ -56,7 +56,7 @@ def test_packed_layouts_match_the_header(tmp_path):
 
 # ---------------------------------------------------------------- convolution
 
-def conv(lib, fn="fwd", dims=(2, 16, 4, BF16), T=64, x=rows(), w=P, bias=P, state=P, y=rows(),
+def conv(lib, fn="fwd", dims=(2, 16, 4, BF16), T=64, x=rows(P + 0x8000), w=P, bias=P, state=P, y=rows(),
          flags=0, seqlens=None):
     d = bytes(m3.m3_conv_dims(*dims))
     if fn == "step":
@@ -97,6 +97,7 @@ def test_conv_prompt_refusals(lib):
     assert conv(lib, y=rows(bs=32, ts=16)) == m3.M3_ERR_SHAPE   # sequences overlap
     assert conv(lib, y=rows(bs=0, ts=16)) == m3.M3_ERR_SHAPE
     assert conv(lib, seqlens=P + 2) == m3.M3_ERR_ALIGN
+    assert conv(lib, x=rows(), y=rows()) == m3.M3_ERR_UNSUPPORTED       # in place
     assert conv(lib, T=0, x=None, y=None) == m3.M3_OK           # no tokens: nothing to do
 
 
@@ -105,14 +106,18 @@ def test_conv_backward_refusals(lib):
     need = m3.m3_conv_bwd_workspace_bytes(d, 64)
     assert need >= 4 * 2 * 5 * 16
 
-    def bwd(dx=(P, 1024, 16), dw=P, db=P, ds=P, dy=rows(), ws=WS, nb=need, bias=P, T=64):
+    Q, R = P + 0x8000, P + 0x10000
+
+    def bwd(dx=(P, 1024, 16), dw=P, db=P, ds=P, dy=rows(Q), ws=WS, nb=need, bias=P, T=64):
         g = bytes(m3.m3_conv_grads(m3.m3_rows(*dx), dw, db, ds))
-        return lib.m3_conv_bwd(bytes(d.c()), T, rows(), P, bias, None, P, dy, g, ws, nb, 0, None)
+        return lib.m3_conv_bwd(bytes(d.c()), T, rows(R), P, bias, None, P, dy, g, ws, nb, 0, None)
 
     assert bwd(dw=0) == m3.M3_ERR_NULL
     assert bwd(db=0) == m3.M3_ERR_NULL
     assert bwd(dx=(0, 1024, 16)) == m3.M3_ERR_NULL
     assert bwd(dx=(P, 16, 16)) == m3.M3_ERR_SHAPE
+    assert bwd(dx=(Q, 1024, 16)) == m3.M3_ERR_UNSUPPORTED        # dx over dy
+    assert bwd(dx=(R, 1024, 16)) == m3.M3_ERR_UNSUPPORTED        # dx over x
     assert bwd(dy=rows(0)) == m3.M3_ERR_NULL
     assert bwd(ds=P + 2) == m3.M3_ERR_ALIGN
     assert bwd(ws=0) == m3.M3_ERR_WORKSPACE
