@@ -582,9 +582,10 @@ m3_status m3_sel_bwd(const m3_sel_dims* dims, int32_t seqlen, const m3_sel_input
  *            no residual x itself (same pointer and stride)
  *   weight   [width] fp32 or NULL (ones)
  *   y        M3_OUT_IO: [rows][width] io dtype; may be x itself (same pointer and stride).
- *            M3_OUT_E4M3: [rows][width] e4m3 bytes, q = round(y / scale) with one fp32 scale for
- *            each 128 consecutive values of a row (the last group may be shorter),
- *            scale = max(max |y|, 2^-100) / 448, in scales [rows][ceil(width / 128)], packed.
+ *            M3_OUT_E4M3: [rows][width] e4m3 bytes, with one fp32 scale for each 128 consecutive
+ *            values of a row (the last group may be shorter), in scales [rows][ceil(width / 128)],
+ *            packed: scale = max(max |y|, 2^-100) / 448, and q is the e4m3 value nearest to
+ *            y / scale (ties to even) before either is rounded; with the floor, y is rounded.
  *            y stands for q * scale.  A group that holds a NaN or an infinity has a NaN scale.
  * Strides are in elements and at least width.  width is at most 32768.  eps >= 0
  * (M3_ERR_SHAPE otherwise).  rows 0 does nothing.  No workspace.

@@ -54,6 +54,89 @@ __device__ __forceinline__ void row_sum(float (&v)[M], float* sm) {
     }
 }
 
+__device__ __forceinline__ uint2 to_e4m3(const float (&q)[8]) {
+    union { __nv_fp8x2_storage_t h[4]; uint2 v; } out;
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+        out.h[j] = __nv_cvt_float2_to_fp8x2(make_float2(q[2 * j], q[2 * j + 1]), __NV_SATFINITE, __NV_E4M3);
+    return out.v;
+}
+
+// Eight values of a row in e4m3, with the scale of their group of 128 (16 neighbouring lanes).
+//
+// A value next to the middle of two steps lands on the other step for an error of one ulp.  The
+// reciprocal root is a factor of y and of max |y| alike, so the quotient is 448 r w / max |r w|;
+// with the products, the reciprocal of their largest and the quotient each rounded once, t is
+// within 2^-23 of it.  Where t (1 - 2^-22) and t (1 + 2^-22) go to the same step, so does the
+// quotient.  Else (about one warp in six hundred) it is compared with g, the nearest value of five
+// significant bits (every step and every middle of two is one): 448 r w - g max |r w| is exact in
+// 64 bits, and its sign says on which side of g the quotient is rounded.  So every value is the
+// nearest step, ties to even; y / scale from rounded y and scale put 40 of 67 million on the other
+// step, and took longer (122 us for 32768 rows of 2048 among others of their kind, now 119).
+template <bool WIDE>
+__device__ __forceinline__ void store_e4m3(const float (&r)[8], const float (&w)[8], float mean, float rstd,
+                                           uint8_t* o, int n, float* scale_out) {
+    // rstd = ratio 2^e: the power of two keeps the products in range and rounds nothing
+    const uint32_t bits = __float_as_uint(rstd);
+    const float pow2 = __uint_as_float(bits & 0x7f800000u);
+    const float ratio = __uint_as_float((bits & 0x007fffffu) | 0x3f800000u);
+    // what the reciprocal root lacks (one Newton step on mean rstd^2 = 1, by FMA), for the scale
+    const float p = mean * rstd, e = fmaf(mean, rstd, -p);
+    float low = 0.5f * ratio * (fmaf(-p, rstd, 1.f) - e * rstd);
+    if (!(fabsf(low) < ratio)) low = 0.f;      // a mean of 0, infinity or NaN has no remainder
+    float hi[8], top = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        hi[j] = __fmul_rn(r[j] * pow2, w[j]);
+        top = max_nan(top, fabsf(hi[j]));        // padding is 0
+    }
+#pragma unroll
+    for (int s = 8; s > 0; s >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, s));
+    const float product = top * ratio;
+    const float amax = product + fmaf(top, low, fmaf(top, ratio, -product));
+    const bool tiny = amax < kAmaxFloor;
+    const float inv = tiny ? ratio * (kE4m3Max / kAmaxFloor) : kE4m3Max / top;
+    if (scale_out) *scale_out = max_nan(amax, kAmaxFloor) / kE4m3Max;
+    constexpr float kSpread = 2.384185791015625e-07f;      // 2^-22
+    float q[8], above[8];
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        const float t = __fmul_rn(hi[j], inv);
+        q[j] = t * (1.f - kSpread);
+        above[j] = t * (1.f + kSpread);
+    }
+    union { uint8_t b[8]; uint2 v; } out;
+    out.v = to_e4m3(q);
+    const uint2 other = to_e4m3(above);
+    const bool apart = out.v.x != other.x || out.v.y != other.y;
+    if (__any_sync(0xffffffffu, apart)) {
+        double largest = 0.;
+#pragma unroll
+        for (int j = 0; j < 8; j++) largest = fmax(largest, fabs((double)(r[j] * pow2) * (double)w[j]));
+#pragma unroll
+        for (int s = 8; s > 0; s >>= 1)
+            largest = fmax(largest, __shfl_xor_sync(0xffffffffu, largest, s));
+        if (tiny) largest = (double)kAmaxFloor / (double)ratio;
+        if (apart) {
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const uint32_t g = (__float_as_uint(fabsf(hi[j] * inv)) + 0x40000u) & ~0x7ffffu;
+                const double y = (double)kE4m3Max * fabs((double)(r[j] * pow2) * (double)w[j]);
+                const double gap = fma(-(double)__uint_as_float(g), largest, y);
+                q[j] = copysignf(__uint_as_float(gap > 0. ? g + 1u : gap < 0. ? g - 1u : g), hi[j]);
+            }
+            out.v = to_e4m3(q);
+        }
+    }
+    if constexpr (WIDE) {
+        if (n > 0) *reinterpret_cast<uint2*>(o) = out.v;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            if (j < n) o[j] = out.b[j];
+    }
+}
+
 template <typename IO, typename RES, int OUT, int TPR, int NV, bool WIDE>
 __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_fwd_kernel(const NormArgs a) {
     constexpr int RPB = TPR < 128 ? 128 / TPR : 1;
@@ -81,53 +164,27 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_fwd_kernel(const N
     }
     row_sum<TPR>(ss, sm);
     const float mean = ss[0] / (float)a.d + a.eps, rstd = 1.f / sqrtf(mean);
-    // In e4m3 an error of one ulp of y that crosses the middle of two steps costs a whole step, so
-    // y = r / sqrt(mean) is formed with the reciprocal root's remainder: rstd + low is it to twice
-    // the digits (one Newton step on mean rstd^2 = 1, the products' low parts by FMA).
-    float low = 0.f;
-    if constexpr (OUT == M3_OUT_E4M3) {
-        const float p = mean * rstd, e = fmaf(mean, rstd, -p);
-        low = 0.5f * rstd * (fmaf(-p, rstd, 1.f) - e * rstd);
-        if (!(fabsf(low) < rstd)) low = 0.f;      // a mean of 0, infinity or NaN has no remainder
-    }
 #pragma unroll
     for (int v = 0; v < NV; v++) {
         const int i = (k + v * TPR) * 8, n = live ? min(max(a.d - i, 0), 8) : 0;
         if (a.res_out)
             Vec<RES, 8>::template store<WIDE>(r[v], static_cast<RES*>(a.res_out) + row * a.ros + i, n);
-        float y[8], w[8];
-        if (a.weight) Vec<float, 8>::load<WIDE>(w, a.weight + i, min(max(a.d - i, 0), 8));
+        float w[8];
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-            y[j] = r[v][j] * rstd;
-            if constexpr (OUT == M3_OUT_E4M3) y[j] += fmaf(r[v][j], low, fmaf(r[v][j], rstd, -y[j]));
-            if (a.weight) y[j] *= w[j];
-        }
+        for (int j = 0; j < 8; j++) w[j] = 1.f;
+        if (a.weight) Vec<float, 8>::load<WIDE>(w, a.weight + i, min(max(a.d - i, 0), 8));
         if constexpr (OUT == M3_OUT_IO) {
+            float y[8];
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                y[j] = r[v][j] * rstd;
+                if (a.weight) y[j] *= w[j];
+            }
             Vec<IO, 8>::template store<WIDE>(y, static_cast<IO*>(a.y) + row * a.ys + i, n);
         } else {
-            float amax = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; j++) amax = max_nan(amax, fabsf(y[j]));   // padding is 0
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            const float scale = max_nan(amax, kAmaxFloor) / kE4m3Max;
-            if (n > 0 && i % 128 == 0) a.scales[row * ((a.d + 127) / 128) + i / 128] = scale;
-            // a rounded division, as the definition has it: one ulp would move values that lie
-            // at the middle of two e4m3 steps
-            union { __nv_fp8x2_storage_t h[4]; uint8_t b[8]; uint2 w; } q;
-#pragma unroll
-            for (int j = 0; j < 4; j++)
-                q.h[j] = __nv_cvt_float2_to_fp8x2(make_float2(y[2 * j] / scale, y[2 * j + 1] / scale),
-                                                  __NV_SATFINITE, __NV_E4M3);
             uint8_t* o = static_cast<uint8_t*>(a.y) + row * a.ys + i;
-            if constexpr (WIDE) {
-                if (n > 0) *reinterpret_cast<uint2*>(o) = q.w;
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; j++)
-                    if (j < n) o[j] = q.b[j];
-            }
+            float* scale = n > 0 && i % 128 == 0 ? a.scales + row * ((a.d + 127) / 128) + i / 128 : nullptr;
+            store_e4m3<WIDE>(r[v], w, mean, rstd, o, n, scale);
         }
     }
 }

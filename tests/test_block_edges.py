@@ -1,0 +1,56 @@
+"""The block operators at the edges of their values: infinities and overflow, steps far below
+one, arguments that are not there."""
+import pytest
+import torch
+
+import block_reference as ref
+import test_block_gpu as tb
+from block_reference import U32, f64, half_step
+from state_space_model_06_b200 import m3
+
+F32 = torch.float32
+
+
+def nearest_e4m3(p, m):
+    """448 p / m rounded to the nearest e4m3 value, ties to even, and how far it lies from the
+    middle of two (relative).  p and m are exact products of two fp32 values: 448 p and a middle
+    (five bits) times m are exact in 64 bits, so the comparison is."""
+    q = 448 * p.abs() / m
+    unit = torch.ldexp(torch.ones_like(q), torch.frexp(q.clamp(min=2.0 ** -6)).exponent - 4)
+    k = torch.floor(q / unit)
+    gap = 448 * p.abs() - (k + 0.5) * unit * m
+    up = torch.where(gap == 0, k % 2 == 1, gap > 0)
+    return torch.copysign((k + up) * unit, p), gap.abs() / (448 * p.abs() + 1e-300)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [2048, 1000])
+@pytest.mark.parametrize("weighted", [True, False])
+def test_norm_e4m3_values_are_the_nearest(weighted, d):
+    """Values next to the middle of two e4m3 steps: each goes to the nearer one, and those in the
+    middle itself (without a weight there are some) to the even one."""
+    rows, n = 96, -(-d // 128)
+    g = torch.Generator().manual_seed(55)
+    x = 2 * torch.randn((rows, d), generator=g)
+    w = 1 + 0.2 * torch.randn(d, generator=g) if weighted else torch.ones(d)
+    p = x.double() * w.double()
+    at = torch.arange(d) // 128
+    pad = torch.zeros(rows, n * 128, dtype=torch.float64)
+    pad[:, :d] = p.abs()
+    top, where = pad.view(rows, n, 128).max(-1)
+    # every other value of a group is the fp32 value next to a middle of two steps
+    keep = torch.zeros(rows, n * 128, dtype=torch.bool)
+    keep.scatter_(1, where + 128 * torch.arange(n), True)
+    steps = torch.arange(8, 16).double() + 0.5
+    middle = steps[torch.randint(0, 8, (rows, d), generator=g)] * \
+        2.0 ** torch.randint(-9, 5, (rows, d), generator=g)
+    near = (middle * top[:, at] / 448 / w.double()).float()
+    x = torch.where(keep[:, :d], x, torch.copysign(near, x))
+    want, gap = nearest_e4m3(x.double() * w.double(), top[:, at])
+    assert (gap < 2.0 ** -22).sum() > 0.9 * rows * d
+    dims = m3.NormDims(rows, d, m3.M3_F32, m3.M3_F32, m3.M3_OUT_E4M3)
+    q = torch.empty(rows, d, dtype=torch.float8_e4m3fn, device="cuda")
+    m3.m3_norm_fwd(dims, x.cuda(), None, w.cuda() if weighted else None, 1e-6, q,
+                   m3.alloc_norm_scales(dims))
+    got = f64(q.float())
+    assert torch.equal(got, want), int((got != want).sum())
