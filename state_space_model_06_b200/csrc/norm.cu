@@ -68,14 +68,20 @@ __device__ __forceinline__ uint2 to_e4m3(const float (&q)[8]) {
 // reciprocal root is a factor of y and of max |y| alike, so the quotient is 448 r w / max |r w|;
 // with the products, the reciprocal of their largest and the quotient each rounded once, t is
 // within 2^-23 of it.  Where t (1 - 2^-22) and t (1 + 2^-22) go to the same step, so does the
-// quotient.  Else (about one warp in six hundred) it is compared with g, the nearest value of five
-// significant bits (every step and every middle of two is one): 448 r w - g max |r w| is exact in
-// 64 bits, and its sign says on which side of g the quotient is rounded.  So every value is the
-// nearest step, ties to even; y / scale from rounded y and scale put 40 of 67 million on the other
-// step, and took longer (122 us for 32768 rows of 2048 among others of their kind, now 119).
-template <bool WIDE>
-__device__ __forceinline__ void store_e4m3(const float (&r)[8], const float (&w)[8], float mean, float rstd,
-                                           uint8_t* o, int n, float* scale_out) {
+// quotient.  Else (one warp in six hundred) it is compared with g, the nearest value of five
+// significant bits (every step and every middle of two is one): the sign of 448 r w - g max |r w|
+// says on which side of g the quotient is rounded.  It is formed by FMA, the products' low parts
+// added where there are weights, exactly without them and to 2^-44 with them.
+// bf16 values without weights (SHORT) lie in the middle itself in most warps, else 2^-13 from it
+// (7 a and g b are integers below 2^13 for 8-bit a and b): one remainder step makes t the quotient
+// where that is representable, and the conversion does the rest (32768 rows of 2048: 74 us; 91
+// by the comparison).
+// So every value is the nearest step, ties to even; y / scale from rounded y and scale put 40 of 67
+// million on the other step, and took longer (122 us for 32768 rows of 2048 with an fp32 residual,
+// among others of their kind; now 118).
+template <bool WIDE, bool SHORT>
+__device__ __forceinline__ void store_e4m3(const float (&r)[8], const float (&w)[8], bool weighted, float mean,
+                                           float rstd, uint8_t* o, int n, float* scale_out) {
     // rstd = ratio 2^e: the power of two keeps the products in range and rounds nothing
     const uint32_t bits = __float_as_uint(rstd);
     const float pow2 = __uint_as_float(bits & 0x7f800000u);
@@ -97,35 +103,56 @@ __device__ __forceinline__ void store_e4m3(const float (&r)[8], const float (&w)
     const bool tiny = amax < kAmaxFloor;
     const float inv = tiny ? ratio * (kE4m3Max / kAmaxFloor) : kE4m3Max / top;
     if (scale_out) *scale_out = max_nan(amax, kAmaxFloor) / kE4m3Max;
-    constexpr float kSpread = 2.384185791015625e-07f;      // 2^-22
-    float q[8], above[8];
-#pragma unroll
-    for (int j = 0; j < 8; j++) {
-        const float t = __fmul_rn(hi[j], inv);
-        q[j] = t * (1.f - kSpread);
-        above[j] = t * (1.f + kSpread);
-    }
     union { uint8_t b[8]; uint2 v; } out;
-    out.v = to_e4m3(q);
-    const uint2 other = to_e4m3(above);
-    const bool apart = out.v.x != other.x || out.v.y != other.y;
-    if (__any_sync(0xffffffffu, apart)) {
-        double largest = 0.;
+    float q[8];
+    if (SHORT && !weighted) {
+        const float back = tiny ? 0.f : inv * (1.f / kE4m3Max);
 #pragma unroll
-        for (int j = 0; j < 8; j++) largest = fmax(largest, fabs((double)(r[j] * pow2) * (double)w[j]));
+        for (int j = 0; j < 8; j++) {
+            const float t = __fmul_rn(hi[j], inv);
+            q[j] = fmaf(fmaf(-t, top, kE4m3Max * hi[j]), back, t);
+        }
+        out.v = to_e4m3(q);
+    } else {
+        constexpr float kSpread = 2.384185791015625e-07f;      // 2^-22
+        float above[8];
 #pragma unroll
-        for (int s = 8; s > 0; s >>= 1)
-            largest = fmax(largest, __shfl_xor_sync(0xffffffffu, largest, s));
-        if (tiny) largest = (double)kAmaxFloor / (double)ratio;
-        if (apart) {
+        for (int j = 0; j < 8; j++) {
+            const float t = __fmul_rn(hi[j], inv);
+            q[j] = t * (1.f - kSpread);
+            above[j] = t * (1.f + kSpread);
+        }
+        out.v = to_e4m3(q);
+        const uint2 other = to_e4m3(above);
+        const uint32_t apart[2] = {out.v.x ^ other.x, out.v.y ^ other.y};      // a byte a value
+        if (__any_sync(0xffffffffu, apart[0] | apart[1])) {
+            // the low part of the largest product
+            float top_lo = 0.f;
+            if (weighted && !__all_sync(0xffffffffu, tiny)) {
+                top_lo = -3.4e38f;
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+                    if (fabsf(hi[j]) == top)
+                        top_lo = fmaxf(top_lo, fmaf(fabsf(r[j] * pow2), fabsf(w[j]), -fabsf(hi[j])));
+#pragma unroll
+                for (int s = 8; s > 0; s >>= 1) top_lo = fmaxf(top_lo, __shfl_xor_sync(0xffffffffu, top_lo, s));
+            }
+            if (tiny) {
+                top = kAmaxFloor / ratio;
+                top_lo = 0.f;
+            }
 #pragma unroll
             for (int j = 0; j < 8; j++) {
-                const uint32_t g = (__float_as_uint(fabsf(hi[j] * inv)) + 0x40000u) & ~0x7ffffu;
-                const double y = (double)kE4m3Max * fabs((double)(r[j] * pow2) * (double)w[j]);
-                const double gap = fma(-(double)__uint_as_float(g), largest, y);
-                q[j] = copysignf(__uint_as_float(gap > 0. ? g + 1u : gap < 0. ? g - 1u : g), hi[j]);
+                if (!(apart[j / 4] & (0xffu << (j % 4 * 8)))) continue;
+                // 2^-9 on both sides keeps the products in range
+                const float h = fabsf(hi[j]);
+                const uint32_t g = (__float_as_uint(h * inv) + 0x40000u) & ~0x7ffffu;
+                const float step = __uint_as_float(g) * 0.001953125f, x = __fmul_rn(step, top);
+                float gap = fmaf(0.875f, h, -x) - fmaf(step, top, -x);
+                if (weighted) gap += fmaf(0.875f, fmaf(fabsf(r[j] * pow2), fabsf(w[j]), -h), -(step * top_lo));
+                const float side = __uint_as_float(gap > 0.f ? g + 1u : gap < 0.f ? g - 1u : g);
+                out.b[j] = __nv_cvt_float_to_fp8(copysignf(side, hi[j]), __NV_SATFINITE, __NV_E4M3);
             }
-            out.v = to_e4m3(q);
         }
     }
     if constexpr (WIDE) {
@@ -184,7 +211,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_fwd_kernel(const N
         } else {
             uint8_t* o = static_cast<uint8_t*>(a.y) + row * a.ys + i;
             float* scale = n > 0 && i % 128 == 0 ? a.scales + row * ((a.d + 127) / 128) + i / 128 : nullptr;
-            store_e4m3<WIDE>(r[v], w, mean, rstd, o, n, scale);
+            store_e4m3<WIDE, sizeof(RES) == 2>(r[v], w, a.weight != nullptr, mean, rstd, o, n, scale);
         }
     }
 }
