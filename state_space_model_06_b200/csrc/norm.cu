@@ -99,9 +99,10 @@ __device__ __forceinline__ void store_e4m3(const float (&r)[8], const float (&w)
 #pragma unroll
     for (int s = 8; s > 0; s >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, s));
     const float product = top * ratio;
-    const float amax = product + fmaf(top, low, fmaf(top, ratio, -product));
+    float amax = product + fmaf(top, low, fmaf(top, ratio, -product));
     const bool tiny = amax < kAmaxFloor;
-    const float inv = tiny ? ratio * (kE4m3Max / kAmaxFloor) : kE4m3Max / top;
+    float inv = tiny ? ratio * (kE4m3Max / kAmaxFloor) : kE4m3Max / top;
+    if (!(amax < __int_as_float(0x7f800000))) amax = inv = __int_as_float(0x7fffffff);   // infinite or NaN: all NaN
     if (scale_out) *scale_out = max_nan(amax, kAmaxFloor) / kE4m3Max;
     union { uint8_t b[8]; uint2 v; } out;
     float q[8];

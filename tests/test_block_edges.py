@@ -76,3 +76,28 @@ def test_norm_e4m3_of_short_values(d, residual):
     m3.m3_norm_fwd(dims, x.cuda(), None if res is None else res.cuda(), None, 1e-6, q,
                    m3.alloc_norm_scales(dims))
     assert torch.equal(f64(q.float()), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [512, 500])
+def test_norm_infinite_products_have_nan_scales(d):
+    """An infinite weight, and a product of finite factors that overflows: the group holds an
+    infinity, so its scale is NaN, in wide rows and narrow ones; the other groups are as without."""
+    g = torch.Generator().manual_seed(51)
+    x, w = torch.randn((3, d), generator=g).cuda(), 1 + torch.rand(d, generator=g).cuda()
+    dims = m3.NormDims(3, d, m3.M3_F32, m3.M3_F32, m3.M3_OUT_E4M3)
+
+    def run(w):
+        q = torch.empty(3, d, dtype=torch.float8_e4m3fn, device="cuda")
+        sc = m3.alloc_norm_scales(dims)
+        m3.m3_norm_fwd(dims, x, None, w, 1e-6, q, sc)
+        return q.float(), sc
+
+    x[:, 130], x[:, 300] = 4.0, 0.5
+    q0, s0 = run(w)
+    w[130] = 3.0e38                  # y = 4 / rms * 3e38 is past the largest fp32 value
+    w[300] = float("-inf")
+    q, sc = run(w)
+    assert torch.isnan(sc[:, 1:3]).all() and torch.isnan(q[:, 128:384]).all()
+    assert torch.equal(sc[:, [0, 3]], s0[:, [0, 3]])
+    assert torch.equal(q[:, :128], q0[:, :128]) and torch.equal(q[:, 384:], q0[:, 384:])
