@@ -538,6 +538,8 @@ def _bad(status, name, t, what):
 
 def _device(t, name):
     """The index of a call's device: that of its first tensor."""
+    if t is None:
+        raise M3Error(M3_ERR_NULL, name)
     dev = t.get_device()
     if dev < 0:
         _bad(M3_ERR_UNSUPPORTED, name, t, "a CUDA tensor")

@@ -101,3 +101,17 @@ def test_norm_infinite_products_have_nan_scales(d):
     assert torch.isnan(sc[:, 1:3]).all() and torch.isnan(q[:, 128:384]).all()
     assert torch.equal(sc[:, [0, 3]], s0[:, [0, 3]])
     assert torch.equal(q[:, :128], q0[:, :128]) and torch.equal(q[:, 384:], q0[:, 384:])
+
+
+def test_binding_names_what_is_missing():
+    """A call's first tensor decides its device: without it the call ends as with any other
+    argument that is needed and not there."""
+    for call in (lambda: m3.m3_conv_fwd(m3.ConvDims(1, 8, 4), 3, *[None] * 5),
+                 lambda: m3.m3_conv_step(m3.ConvDims(1, 8, 4), *[None] * 5),
+                 lambda: m3.m3_sel_fwd(m3.SelDims(1, 8, 1, 4), 3, *[None] * 11),
+                 lambda: m3.m3_sel_step(m3.SelDims(1, 8, 1, 4), *[None] * 10),
+                 lambda: m3.m3_norm_fwd(m3.NormDims(2, 8), None, None, None, 1e-6, None),
+                 lambda: m3.m3_norm_bwd(m3.NormDims(2, 8), None, None, 1e-6, *[None] * 6)):
+        with pytest.raises(m3.M3Error) as e:
+            call()
+        assert e.value.status == m3.M3_ERR_NULL
