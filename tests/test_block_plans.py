@@ -1,0 +1,207 @@
+"""The block operators under the plans that large calls get: segments of several tiles in the
+selective scan, long runs in the convolution, many turns of a block in the norm's backward.  Many
+short sequences (or rows) reach them at sizes that a 64-bit reference can follow.  The plans are
+restated here and held against the library's workspace sizes, so that no case can fall back to a
+simpler plan unnoticed."""
+import pytest
+import torch
+
+import block_reference as ref
+import test_block_gpu as tb
+from block_reference import U32, f64, half_step
+from state_space_model_06_b200 import m3
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def round256(n):
+    return -(-n // 256) * 256
+
+
+def ends(b, T, marks):
+    """Lengths that end at every mark in turn, among them 0, 1 and beyond both sides."""
+    marks = [T, 0, 1, T + 9, -3] + list(marks)
+    return torch.tensor([marks[i % len(marks)] for i in range(b)], dtype=torch.int32).cuda()
+
+
+def lay(t, wide):
+    """The same values in rows that start on 16 bytes, or off them."""
+    if wide:
+        return t.contiguous()
+    out = torch.empty(*t.shape[:2], t[0, 0].numel() + 1, dtype=t.dtype, device=t.device)
+    out = out[..., 1:].unflatten(-1, t.shape[2:]) if t.dim() > 3 else out[..., 1:]
+    return out.copy_(t)
+
+
+def cells(b, T, ch, G, N, io, marks, wide, seed):
+    """Inputs of a scan, with NaN behind the lengths, and the same in 64 bits with zeros there."""
+    c, _, _ = tb.scan_inputs((b, T, ch, G, N, io, "z D bias softplus"), seed)
+    for k in ("x", "dt", "B", "C", "z"):
+        c[k] = lay(c[k], wide)
+    sl = ends(b, T, marks)
+    past = torch.arange(T).cuda()[None] >= sl[:, None]
+    for k in ("x", "dt", "B", "C", "z"):
+        c[k].masked_fill_(past.view(b, T, *[1] * (c[k].dim() - 2)), float("nan"))
+    r = {k: f64(v) for k, v in c.items()}
+    for k in ("x", "dt", "B", "C", "z"):
+        r[k].nan_to_num_(nan=0.0)
+    return c, r, sl
+
+
+# ---------------------------------------------------------------- scan, backward
+
+# states: tokens of a tile, channels of a block, padded states
+BWD_SHAPE = {4: (32, 64, 4), 8: (32, 64, 8), 16: (32, 64, 16), 24: (32, 32, 32), 40: (32, 16, 64),
+             72: (16, 16, 128), 200: (16, 8, 256)}
+
+
+def bwd_plan(b, T, ch, G, N, m=None):
+    """Tiles of a segment (or m of them), segments, and the workspace's bytes."""
+    tile, CB, NP = BWD_SHAPE[N]
+    blocks, ntile = -(-(ch // G) // CB) * G, -(-T // tile)
+    if m is None:
+        m = 4
+        while m > 1 and blocks * b * -(-ntile // m) < 148 * 12:
+            m //= 2
+    nseg, states = -(-ntile // m), ch * N
+    sizes = [b * ntile * states, b * ntile * ch] + [b * nseg * states] * 3 + \
+        [b * nseg * 2 * ch, b * T * blocks * 2 * NP]
+    return m, nseg, sum(round256(4 * n) for n in sizes)
+
+
+SCAN_BWD = [  # b, tiles' worth of tokens and a few more, ch, G, N, io, wide rows, tiles a segment
+    (890, 4, 8, 1, 4, BF, True, 4),
+    (600, 4, 5, 1, 4, F32, False, 2),
+    (890, 4, 4, 1, 8, F32, True, 4),
+    (600, 4, 8, 1, 8, BF, True, 2),
+    (890, 4, 8, 1, 16, BF, True, 4),
+    (890, 4, 7, 1, 16, BF, False, 4),
+    (600, 4, 4, 1, 16, F32, True, 2),
+    (450, 4, 6, 2, 16, F32, False, 4),
+    (450, 6, 16, 2, 16, BF, True, 4),       # segments of 4 and 3 tiles
+    (890, 4, 4, 1, 24, F32, True, 4),
+    (600, 4, 8, 1, 24, BF, True, 2),
+    (890, 4, 3, 1, 40, BF, False, 4),
+    (600, 4, 4, 1, 40, F32, True, 2),
+    (890, 4, 8, 1, 72, BF, True, 4),
+    (600, 4, 3, 1, 72, F32, False, 2),
+    (890, 4, 4, 1, 200, F32, True, 4),
+    (600, 4, 5, 1, 200, BF, False, 2),
+]
+
+
+def bwd_tokens(case):
+    b, tiles, ch, G, N, io, wide, m = case
+    return BWD_SHAPE[N][0] * tiles + 5
+
+
+@pytest.mark.parametrize("case", SCAN_BWD)
+def test_scan_bwd_plan(case):
+    """The case gets the segments that it is listed for, by the library's own workspace size."""
+    b, _, ch, G, N, io, _, want = case
+    T = bwd_tokens(case)
+    m, nseg, size = bwd_plan(b, T, ch, G, N)
+    assert m == want and nseg >= 2
+    d = m3.SelDims(b, ch, G, N, m3.io_dtype_of(io))
+    assert m3.m3_sel_bwd_workspace_bytes(d, T) == size
+    # and no other number of tiles a segment would have this size
+    assert all(size != bwd_plan(b, T, ch, G, N, k)[2] for k in (1, 2, 4) if k != m)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", SCAN_BWD)
+def test_scan_bwd_over_several_tiles(case):
+    """Segments of two and four tiles, the last one shorter, with lengths that end in each of
+    them; and the same calls' outputs."""
+    b, _, ch, G, N, io, wide, _ = case
+    T, tile = bwd_tokens(case), BWD_SHAPE[N][0]
+    m, nseg, size = bwd_plan(b, T, ch, G, N)
+    marks = [k * tile + o for k in range(-(-T // tile)) for o in (0, 1, 7, tile - 1)]
+    c, r, sl = cells(b, T, ch, G, N, io, [v for v in marks if 1 < v < T], wide, 31)
+    g = torch.Generator().manual_seed(32)
+    dy, dhT = tb.rnd(g, b, T, ch, dtype=io), tb.rnd(g, b, ch, N)
+    rdy = f64(dy)
+    past = torch.arange(T)[None] >= sl.cpu()[:, None]
+    dy.masked_fill_(past.cuda()[..., None], float("inf"))
+    rdy.masked_fill_(past[..., None], 0.0)
+    dy = lay(dy, wide)
+    lens = ref.lengths(sl, b, T)
+    want = ref.scan_bwd(*r.values(), lens, True, rdy, f64(dhT))
+    mag = ref.scan_bwd(*r.values(), lens, True, rdy, f64(dhT), absolute=True)
+    rel = 2 * ref.scan_bounds(T, N, ch, r["A"], r["dt"], r["bias"], True) + 2.0 ** -19
+    # roundings in a row of a parameter's sum: a segment's tokens, a warp's share of the segments
+    # (eight warps at least), the lanes and the warps
+    rows = m * tile + b * nseg / 8 + 5 + 32
+    d = m3.SelDims(b, ch, G, N, m3.io_dtype_of(io))
+    gr = {k: tb.nan_like(v) for k, v in m3.alloc_sel_grads(d, T).items()}
+    if not wide:
+        for k in ("dx", "ddt", "dz"):
+            gr[k] = lay(gr[k], False)
+    ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+    m3.m3_sel_bwd(d, T, c["x"], c["dt"], c["A"], c["B"], c["C"], c["D"], c["z"], c["bias"],
+                  c["h"], dy, dhT, gr, ws, seqlens=sl, flags=m3.M3_FLAG_DT_SOFTPLUS)
+    for k, v in gr.items():
+        sums = U32 * (ch if k in ("dB", "dC") else rows if k in ("dA", "dD", "ddt_bias") else 0)
+        tol = (rel + sums) * mag[k] + 1e-37
+        if k in ("dx", "ddt", "dB", "dC", "dz"):
+            tol = tol + half_step(io) * want[k].abs()
+        tb.near(v, want[k], tol, k)
+
+
+# ---------------------------------------------------------------- scan, segmented prompts
+
+# states: channels of a block in one piece, and in segments
+FWD_SHAPE = {4: (64, 64), 8: (64, 64), 16: (32, 64), 24: (32, 32), 40: (32, 32), 72: (16, 16),
+             200: (16, 16)}
+
+
+def fwd_plan(b, T, ch, G, N):
+    """Tiles (of 32 tokens) of a segment, segments, and the workspace's bytes."""
+    one, many = (b * G * -(-(ch // G) // CB) for CB in FWD_SHAPE[N])
+    tiles = -(-T // 32)
+    n = min(148 * 14 // many, tiles) if one <= 148 * 3 and tiles > 4 else 1
+    per = -(-tiles // n)
+    n = -(-tiles // per)
+    return per, n, round256(4 * b * n * ch * (N + 1)) if n > 1 else 256
+
+
+SCAN_FWD = [  # b, T, ch, G, N, io, wide rows
+    (400, 349, 8, 1, 4, BF, True),          # segments of 3, 3, 3 and 2 tiles
+    (400, 349, 4, 1, 8, F32, True),
+    (400, 349, 8, 1, 16, BF, True),
+    (400, 349, 3, 1, 16, F32, False),
+    (100, 352, 4, 4, 24, F32, False),       # four groups of one channel
+    (50, 330, 64, 8, 24, BF, True),
+    (100, 349, 4, 4, 40, BF, False),
+    (100, 349, 16, 4, 72, F32, True),
+    (100, 349, 4, 4, 200, BF, False),
+]
+
+
+@pytest.mark.parametrize("case", SCAN_FWD)
+def test_scan_fwd_plan(case):
+    b, T, ch, G, N, io, _ = case
+    per, n, size = fwd_plan(b, T, ch, G, N)
+    assert per >= 2 and n >= 2
+    assert m3.m3_sel_workspace_bytes(m3.SelDims(b, ch, G, N, m3.io_dtype_of(io)), T) == size
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", SCAN_FWD)
+def test_scan_fwd_over_several_tiles(case):
+    """Segments of several tiles, with lengths that end in each tile of one and at its edges."""
+    b, T, ch, G, N, io, wide = case
+    per, n, size = fwd_plan(b, T, ch, G, N)
+    marks = [k * 32 + o for k in range(-(-T // 32)) for o in (0, 1, 13)]
+    c, r, sl = cells(b, T, ch, G, N, io, [v for v in marks if 1 < v < T], wide, 33)
+    lens = ref.lengths(sl, b, T)
+    want_y, want_h = ref.scan(*r.values(), lens, True)
+    mag_y, mag_h = ref.scan(*r.values(), lens, True, absolute=True)
+    rel = ref.scan_bounds(T, N, ch, r["A"], r["dt"], r["bias"], True)
+    d = m3.SelDims(b, ch, G, N, m3.io_dtype_of(io))
+    y, h = lay(tb.nan_like(c["x"]), wide), c["h"].clone()
+    ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+    m3.m3_sel_fwd(d, T, c["x"], c["dt"], c["A"], c["B"], c["C"], c["D"], c["z"], c["bias"], h, y,
+                  ws, seqlens=sl, flags=m3.M3_FLAG_DT_SOFTPLUS)
+    tb.near(h, want_h, rel * mag_h + 1e-37, "h")
+    tb.near(y, want_y, half_step(io) * want_y.abs() + (rel + 2.0 ** -20) * mag_y + 1e-37, "y")
