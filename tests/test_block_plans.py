@@ -205,3 +205,92 @@ def test_scan_fwd_over_several_tiles(case):
                   ws, seqlens=sl, flags=m3.M3_FLAG_DT_SOFTPLUS)
     tb.near(h, want_h, rel * mag_h + 1e-37, "h")
     tb.near(y, want_y, half_step(io) * want_y.abs() + (rel + 2.0 ** -20) * mag_y + 1e-37, "y")
+
+
+# ---------------------------------------------------------------- convolution
+
+def conv_run(b, T, C, slots):
+    """Tokens of a run: the least time in whole rounds of blocks."""
+    cost = lambda s: -(-(b * -(-C // 512) * -(-T // s)) // slots) * (s + 8)
+    return min(range(8, 129, 8), key=cost)
+
+
+CONV = [  # b, T, C, W, io, options: wide rows with C a multiple of 16 bytes, else narrow ones
+    (590, 230, 64, 4, BF, "silu bias"),
+    (590, 230, 20, 4, F32, "silu bias"),
+    (590, 230, 21, 4, BF, "silu bias"),
+    (590, 230, 12, 3, F32, "bias"),
+    (590, 231, 16, 8, BF, "silu"),
+    (590, 233, 8, 8, F32, "silu bias"),
+    (590, 229, 9, 2, F32, "silu bias odd"),
+    (590, 232, 8, 1, BF, "silu bias"),
+]
+
+
+@pytest.mark.parametrize("case", CONV)
+def test_conv_plan(case):
+    """Runs of several turns of the ring, forward (four groups of four tokens) and backward."""
+    b, T, C, W, io, _ = case
+    assert conv_run(b, T, C, 148 * 7) >= 48
+    s = conv_run(b, T, C, 148 * 4)
+    assert s >= 48
+    assert m3.m3_conv_bwd_workspace_bytes(m3.ConvDims(b, C, W, m3.io_dtype_of(io)), T) == \
+        round256(4 * b * -(-T // s) * (W + 1) * C)
+
+
+def conv_lengths(b, T):
+    """Ends before, at and behind the ring's turns and the groups of four."""
+    return ends(b, T, [2, 3, 4, 5, 11, 15, 16, 17, 18, 19, 47, 55, 56, 57, 63, 64, 71, 72, 73, 74,
+                       75, 76, 79, 100, 112, 144, 145, 168, 190, 200, T - 1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", CONV)
+def test_conv_fwd_long_runs(case):
+    b, T, C, W, io, _ = case
+    x, w, bias, state, _, act = tb.conv_inputs(case, 41)
+    sl = conv_lengths(b, T)
+    x.masked_fill_((torch.arange(T).cuda()[None] >= sl[:, None])[..., None], float("nan"))
+    lens = ref.lengths(sl, b, T)
+    y, new = ref.conv(*(f64(v) for v in (x, w, bias, state)), lens, act)
+    tol = tb.conv_tol(case, (x, w, bias, state), lens, act, y)
+    out = tb.nan_like(torch.empty(b, T, C, dtype=io, device="cuda"))
+    m3.m3_conv_fwd(m3.ConvDims(b, C, W, m3.io_dtype_of(io)), T, x, w, bias, state, out, seqlens=sl,
+                   flags=m3.M3_FLAG_SILU if act else 0)
+    tb.near(out, y, tol, "y")
+    assert torch.equal(f64(state), new)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", CONV)
+def test_conv_bwd_long_runs(case):
+    b, T, C, W, io, _ = case
+    x, w, bias, state, _, act = tb.conv_inputs(case, 42)
+    dy = tb.rnd(torch.Generator().manual_seed(43), b, T, C, dtype=io)
+    sl = conv_lengths(b, T)
+    past = (torch.arange(T).cuda()[None] >= sl[:, None])[..., None]
+    x.masked_fill_(past, float("nan"))
+    dy.masked_fill_(past, float("inf"))
+    lens = ref.lengths(sl, b, T)
+    args = [f64(v) for v in (x, w, bias, state)]
+    want = ref.conv_bwd(*args, lens, act, f64(dy))
+    mag = ref.conv_bwd(*args, lens, act, f64(dy), absolute=True)
+    d = m3.ConvDims(b, C, W, m3.io_dtype_of(io))
+    gr = {k: tb.nan_like(v) for k, v in m3.alloc_conv_grads(d, T).items()}
+    m3.m3_conv_bwd(d, T, x, w, bias, state, dy, gr, m3.alloc_conv_bwd_workspace(d, T), seqlens=sl,
+                   flags=m3.M3_FLAG_SILU if act else 0)
+    # the activation's slope moves with pre's error: |act''| <= 1/2 on (W + 3) U32 |terms|
+    pre = args[1].abs().sum(1).max() * max(float(args[0].nan_to_num().abs().max()),
+                                           float(args[3].abs().max()) if args[3].numel() else 0.0)
+    pre = float(pre) + (0.0 if bias is None else float(args[2].abs().max()))
+    rel = (W + 6) * U32 + (2.0 ** -19 + 0.5 * (W + 3) * U32 * pre * 8 if act else 0)
+    s = conv_run(b, T, C, 148 * 4)
+    for k in ("dx", "dweight", "dbias", "dstate"):
+        if k == "dbias" and bias is None:
+            continue
+        tol = rel * mag[k] + 1e-37
+        if k == "dx":
+            tol = tol + half_step(io) * want[k].abs()
+        elif k != "dstate":      # a run's tokens, a warp's share of the runs, the warps
+            tol = tol + (s + b * -(-T // s) / 8 + 32) * U32 * mag[k]
+        tb.near(gr[k], want[k], tol, k)
