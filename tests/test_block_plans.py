@@ -294,3 +294,44 @@ def test_conv_bwd_long_runs(case):
         elif k != "dstate":      # a run's tokens, a warp's share of the runs, the warps
             tol = tol + (s + b * -(-T // s) / 8 + 32) * U32 * mag[k]
         tb.near(gr[k], want[k], tol, k)
+
+
+# ---------------------------------------------------------------- norm, backward
+
+NORM_BWD = [  # rows, width, io, residual, options: threads a row 32 to 1024, two and four vectors
+    (6001, 250, BF, F32, "w"),
+    (5001, 500, F32, F32, "w"),
+    (2501, 1000, BF, BF, "w"),
+    (1300, 2048, BF, F32, "w"),
+    (800, 4096, F32, BF, "w strided"),
+    (400, 8192, BF, F32, "w"),
+    (400, 16384, BF, BF, "w"),
+    (310, 16390, F32, F32, "w"),
+    (310, 32768, BF, F32, "w"),
+]
+
+
+def norm_blocks(rows, width):
+    t = 32
+    while t < 1024 and t * 8 < width:
+        t *= 2
+    groups = -(-rows // max(128 // t, 1))
+    return groups, min(groups, 148 * (1024 // max(t, 128)))
+
+
+@pytest.mark.parametrize("case", NORM_BWD)
+def test_norm_bwd_plan(case):
+    """Every block takes two turns or more, and some one more than others."""
+    rows, width, io, res, _ = case
+    groups, blocks = norm_blocks(rows, width)
+    # rows that share a block's turn are the spare ones' case too
+    assert groups > blocks and groups % blocks
+    d = m3.NormDims(rows, width, m3.io_dtype_of(io), m3.io_dtype_of(res))
+    assert m3.m3_norm_bwd_workspace_bytes(d) == round256(4 * blocks * width)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("inplace", [False, True])
+@pytest.mark.parametrize("case", NORM_BWD)
+def test_norm_bwd_many_turns(case, inplace):
+    tb.test_norm_bwd(case, inplace)
