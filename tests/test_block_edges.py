@@ -115,3 +115,32 @@ def test_binding_names_what_is_missing():
         with pytest.raises(m3.M3Error) as e:
             call()
         assert e.value.status == m3.M3_ERR_NULL
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("call", ["prompt", "step"])
+def test_scan_step_after_softplus(call):
+    """The step itself: from a zero state, x = B = 1 leave h = delta.
+
+    With U = 2^-24 and v < 0, u = e^v is off by 1.22 |v| U for its argument (the rounded product
+    |v| log2(e), and log2(e) itself) and by 4 U for the hardware's exponential.  s = u / (2 + u)
+    adds 1 U for the sum, 2 U for the reciprocal and 1 U for the product; 2 atanh(s) = log(1 + u)
+    magnifies what has come together so far by at most 1.09 (s <= 1/3), and adds 2 U for the
+    series, its fit and the last sum.  In all (1.33 |v| + 11) U.  For v > 0 the same is relative
+    to the smaller of two positive terms, whose sum rounds once more."""
+    n = 4096
+    v = torch.linspace(-85.0, 40.0, n)
+    dt = v.cuda()
+    want = torch.logaddexp(f64(dt), torch.zeros(1, dtype=torch.float64))
+    one, h = torch.ones(1, n, device="cuda"), torch.zeros(1, n, 1, device="cuda")
+    bc, A = torch.ones(1, 1, 1, device="cuda"), -torch.ones(n, 1, device="cuda")
+    d = m3.SelDims(1, n, 1, 1, m3.M3_F32)
+    y, flags = torch.empty_like(one), m3.M3_FLAG_DT_SOFTPLUS
+    if call == "step":
+        m3.m3_sel_step(d, one, dt[None], A, bc, bc, None, None, None, h, y, flags=flags)
+    else:
+        m3.m3_sel_fwd(d, 1, one[None], dt[None, None], A, bc[None], bc[None], None, None, None, h,
+                      y[None], None, flags=flags)
+    tol = (1.33 * f64(dt).abs() + 12) * U32 * want
+    tb.near(h.view(-1), want, tol, "delta")
+    assert torch.equal(y.view(-1), h.view(-1))
