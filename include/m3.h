@@ -433,7 +433,8 @@ m3_status m3_scan_bwd_ex(const m3_dims* dims, int32_t seqlen, const void* x, con
  *   - Unknown or foreign flags return M3_ERR_UNSUPPORTED, as do more than 2^30 tokens or 2^24
  *     channels.
  *   - Workspaces hold nothing between calls.  Calls that can overlap on the GPU (two streams, two
- *     captured graphs replayed side by side) need a workspace each.
+ *     captured graphs replayed side by side) need a workspace each.  The size for a seqlen serves
+ *     every shorter call of the same dims.
  *   - Sums and states are fp32; each output is rounded once to its type.  Every result is
  *     the same from run to run (no atomics).
  *   - Calls launch on the current device; `stream` must be a stream of it.

@@ -95,6 +95,30 @@ void conv_runs(const m3_conv_dims* d, int32_t T, int slots, int* seg, int* nseg)
 }
 constexpr int kConvFwdSlots = 148 * 7, kConvBwdSlots = 148 * 4;    // blocks an SM holds
 
+// Bytes of the shares of `nseg` runs a sequence.
+size_t conv_bytes(const m3_conv_dims* d, int64_t nseg) {
+    const size_t n = sizeof(float) * (size_t)d->batch * nseg * (d->width + 1) * d->channels;
+    return n < 256 ? 256 : (n + 255) / 256 * 256;
+}
+// The most runs of any length up to T (the choice above does not grow with T).  Runs of s tokens
+// make n of them where they are chosen at the longest such length, min(n s, T): the other choices
+// cost the most there.  They cannot be chosen where s + 8 for each s tokens cost more than runs of
+// 128 in their whole rounds: beyond 136 (1 + slots / columns) / (8 / s - 8 / 128) tokens.
+int64_t conv_most_runs(const m3_conv_dims* d, int32_t T, int slots) {
+    const double columns = (double)d->batch * ((d->channels + 511) / 512);
+    int64_t best = ((int64_t)T + 127) / 128;
+    for (int s = 8; s < 128; s += 8) {
+        const double end = 136. * (1. + slots / columns) / (8. / s - 0.0625) + s;
+        int64_t n = ((end < T ? (int64_t)end : T) + s - 1) / s;
+        for (; n > best; n--) {
+            int seg, nseg;
+            conv_runs(d, n * s < T ? (int32_t)(n * s) : T, slots, &seg, &nseg);
+            if (seg == s) best = n;
+        }
+    }
+    return best;
+}
+
 m3_status conv_common(const m3_conv_dims* d, const Geo& g, const m3_rows* x, const float* weight,
                       const float* bias, const int32_t* seqlens, const void* state, uint32_t flags) {
     if (flags & ~M3_FLAG_SILU) return M3_ERR_UNSUPPORTED;
@@ -178,10 +202,7 @@ m3_status m3_conv_bwd_workspace_bytes(const m3_conv_dims* d, int32_t T, size_t* 
     if (!bytes) return M3_ERR_NULL;
     if (T < 0) return M3_ERR_SHAPE;
     if (T > kMaxTokens) return M3_ERR_UNSUPPORTED;
-    int seg, nseg;
-    conv_runs(d, T, kConvBwdSlots, &seg, &nseg);
-    const size_t n = sizeof(float) * (size_t)d->batch * nseg * (d->width + 1) * d->channels;
-    *bytes = n < 256 ? 256 : (n + 255) / 256 * 256;
+    *bytes = conv_bytes(d, conv_most_runs(d, T, kConvBwdSlots));
     return M3_OK;
 }
 
@@ -213,18 +234,16 @@ m3_status m3_conv_bwd(const m3_conv_dims* d, int32_t T, const m3_rows* x, const 
     if ((st = check_in(*dy, g)) != M3_OK) return st;
     if ((st = check_out(gr->dx, g, d->channels)) != M3_OK) return st;
     if (gr->dx.ptr == x->ptr || gr->dx.ptr == dy->ptr) return M3_ERR_UNSUPPORTED;
-    size_t need;
-    m3_conv_bwd_workspace_bytes(d, T, &need);
-    if (!ws || !at_least(ws, 256) || ws_bytes < need) return M3_ERR_WORKSPACE;
     ConvArgs a;
     conv_args(&a, d, T, x, weight, bias, seqlens, state0, flags);
+    conv_runs(d, T, kConvBwdSlots, &a.seg, &a.nseg);
+    if (!ws || !at_least(ws, 256) || ws_bytes < conv_bytes(d, a.nseg)) return M3_ERR_WORKSPACE;
     a.dy = view(*dy);
     set_out(a.dx, gr->dx);
     a.dweight = gr->dweight;
     a.dbias = bias ? gr->dbias : nullptr;
     a.dstate = gr->dstate;
     a.part = static_cast<float*>(ws);
-    conv_runs(d, T, kConvBwdSlots, &a.seg, &a.nseg);
     if ((int64_t)a.batch * a.nseg > kMaxBlocks) return M3_ERR_UNSUPPORTED;
     a.wide = conv_wide(d, weight, state0) && wide_rows(*x, g) && wide_rows(*dy, g) && wide_rows(gr->dx, g);
     return status_of(launch_conv(a, ConvCall::bwd, d->io_dtype, s));
@@ -307,7 +326,7 @@ m3_status m3_sel_workspace_bytes(const m3_sel_dims* d, int32_t T, size_t* bytes)
     if (!bytes) return M3_ERR_NULL;
     if (T < 0) return M3_ERR_SHAPE;
     if (T > kMaxTokens) return M3_ERR_UNSUPPORTED;
-    const size_t n = T ? sel_fwd_workspace(d->batch, T, d->channels, d->ngroups, d->dstate) : 0;
+    const size_t n = T ? sel_fwd_most(d->batch, T, d->channels, d->ngroups, d->dstate) : 0;
     *bytes = n < 256 ? 256 : (n + 255) / 256 * 256;
     return M3_OK;
 }
@@ -371,7 +390,7 @@ m3_status m3_sel_bwd_workspace_bytes(const m3_sel_dims* d, int32_t T, size_t* by
     SelArgs a;
     std::memset(&a, 0, sizeof(a));
     a.batch = d->batch; a.T = T; a.D = d->channels; a.G = d->ngroups; a.N = d->dstate;
-    const size_t n = sel_bwd_plan(&a, nullptr);
+    const size_t n = sel_bwd_most(a);
     *bytes = n < 256 ? 256 : n;
     return M3_OK;
 }

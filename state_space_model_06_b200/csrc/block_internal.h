@@ -66,10 +66,12 @@ struct SelArgs {
 constexpr int kSelTile = 32;
 int sel_fwd_segments(int batch, int T, int D, int G, int N, int* seg);
 size_t sel_fwd_workspace(int batch, int T, int D, int G, int N);
+size_t sel_fwd_most(int batch, int T, int D, int G, int N);      // of any length up to T
 cudaError_t launch_sel_fwd(const SelArgs& a, int io_dtype, cudaStream_t s);
 cudaError_t launch_sel_step(const SelArgs& a, int io_dtype, cudaStream_t s);
 // Fills in seg, nseg and the workspace pointers (relative to a null workspace: sizes alone).
 size_t sel_bwd_plan(SelArgs* a, char* ws);
+size_t sel_bwd_most(SelArgs a);      // the largest size of any length up to a.T
 cudaError_t launch_sel_bwd(const SelArgs& a, int io_dtype, cudaStream_t s);
 
 // ------------------------------------------------------------------ norm

@@ -660,21 +660,30 @@ cudaError_t by_n(int N, F f) {
 
 }  // namespace
 
-size_t sel_bwd_plan(SelArgs* a, char* ws) {
-    int NP = 0, CB = 0;
-    by_n(a->N, [&](auto sh) {
-        using SH = decltype(sh);
-        a->tile = SH::L;
-        NP = SH::NP;
-        CB = SH::CB;
+// Blocks of channels, and how many blocks the segments must make before they get more tiles.
+static long long sel_bwd_blocks(const SelArgs& a) {
+    int CB = 0;
+    by_n(a.N, [&](auto sh) {
+        CB = decltype(sh)::CB;
         return cudaSuccess;
     });
-    const size_t blks = sel_tiles(a->D, a->G, CB);
+    return sel_tiles(a.D, a.G, CB);
+}
+constexpr long long kBwdBlocks = 148 * 12;
+
+size_t sel_bwd_plan(SelArgs* a, char* ws) {
+    int NP = 0;
+    by_n(a->N, [&](auto sh) {
+        a->tile = decltype(sh)::L;
+        NP = decltype(sh)::NP;
+        return cudaSuccess;
+    });
+    const size_t blks = sel_bwd_blocks(*a);
     a->ntile = (a->T + a->tile - 1) / a->tile;
     // Tiles of a segment: four where the segments still give every SM its blocks several times
     // over (fewer segments are chained, and fewer shares of dA summed), else fewer.
     int m = 4;
-    while (m > 1 && (long long)blks * a->batch * ((a->ntile + m - 1) / m) < 148 * 12) m /= 2;
+    while (m > 1 && (long long)blks * a->batch * ((a->ntile + m - 1) / m) < kBwdBlocks) m /= 2;
     a->seg = m * a->tile;
     a->nseg = (a->ntile + m - 1) / m;
     const size_t runs = (size_t)a->batch * a->nseg, states = (size_t)a->D * a->N;
@@ -693,6 +702,22 @@ size_t sel_bwd_plan(SelArgs* a, char* ws) {
     a->pD = take(runs * 2 * a->D);
     a->pBC = take((size_t)a->batch * a->T * blks * 2 * NP);
     return at;
+}
+
+// The size grows with T but where a segment gets more tiles: the longest length with each number
+// of tiles a segment is looked at.
+size_t sel_bwd_most(SelArgs a) {
+    size_t most = sel_bwd_plan(&a, nullptr);
+    const int tile = a.tile, ntile = a.ntile;
+    const long long columns = (long long)a.batch * sel_bwd_blocks(a), segments = (kBwdBlocks - 1) / columns;
+    for (int m = 1; m < 4; m *= 2) {
+        const long long tiles = 2 * m * segments;      // the most that 2 m a segment are too few for
+        if (tiles < 1 || tiles >= ntile) continue;
+        a.T = (int)tiles * tile;
+        const size_t n = sel_bwd_plan(&a, nullptr);
+        if (n > most) most = n;
+    }
+    return most;
 }
 
 cudaError_t launch_sel_bwd(const SelArgs& a, int io_dtype, cudaStream_t s) {

@@ -446,27 +446,34 @@ cudaError_t step_t(const SelArgs& a, cudaStream_t s) {
 // pass would leave more than half of the GPU idle: then as many segments as fill it about twice (14
 // blocks an SM: 378 us for 16384 tokens of 2048 channels, 397 with 8), down to one tile of tokens
 // each (3 x 509 tokens of 1001 channels: 37 us, 39 with two tiles at least).
-int sel_fwd_segments(int batch, int T, int D, int G, int N, int* seg) {
+static int sel_fwd_most_segments(int batch, int T, int D, int G, int N) {
     auto blocks = [&](bool segments) {
         const int CB = fwd_shape(N, segments, [](auto sh) { return decltype(sh)::CB; });
         return (long long)batch * sel_tiles(D, G, CB);
     };
     const int tiles = (T + kSelTile - 1) / kSelTile;
-    int n = 1;
-    if (blocks(false) <= 148 * 3 && tiles > 4) {
-        const long long want = 148 * 14 / blocks(true);
-        n = want > tiles ? tiles : (int)want;
-        if (n < 1) n = 1;
-    }
+    if (blocks(false) > 148 * 3 || tiles <= 4) return 1;
+    const long long want = 148 * 14 / blocks(true);
+    return want > tiles ? tiles : (int)want;
+}
+int sel_fwd_segments(int batch, int T, int D, int G, int N, int* seg) {
+    const int n = sel_fwd_most_segments(batch, T, D, G, N), tiles = (T + kSelTile - 1) / kSelTile;
     const int per = (tiles + n - 1) / n;
     *seg = per * kSelTile;
     return (tiles + per - 1) / per;
 }
 
+static size_t sel_fwd_bytes(int n, int batch, int D, int N) {
+    return n > 1 ? sizeof(float) * (size_t)batch * n * D * (N + 1) : 0;
+}
 size_t sel_fwd_workspace(int batch, int T, int D, int G, int N) {
     int seg;
-    const int n = sel_fwd_segments(batch, T, D, G, N, &seg);
-    return n > 1 ? sizeof(float) * (size_t)batch * n * D * (N + 1) : 0;
+    return sel_fwd_bytes(sel_fwd_segments(batch, T, D, G, N, &seg), batch, D, N);
+}
+// Whole tiles leave some lengths with fewer segments than shorter ones: the number before that
+// grows with T.
+size_t sel_fwd_most(int batch, int T, int D, int G, int N) {
+    return sel_fwd_bytes(sel_fwd_most_segments(batch, T, D, G, N), batch, D, N);
 }
 
 cudaError_t launch_sel_fwd(const SelArgs& a, int io_dtype, cudaStream_t s) {

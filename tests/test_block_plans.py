@@ -69,6 +69,16 @@ def bwd_plan(b, T, ch, G, N, m=None):
     return m, nseg, sum(round256(4 * n) for n in sizes)
 
 
+def bwd_serves(b, T, ch, G, N):
+    """The size that serves every length up to T: that of T itself, or of the longest with fewer
+    tiles a segment."""
+    tile = BWD_SHAPE[N][0]
+    longest = {}
+    for n in range(1, -(-T // tile) + 1):
+        longest[bwd_plan(b, n * tile, ch, G, N)[0]] = min(n * tile, T)
+    return max(bwd_plan(b, t, ch, G, N)[2] for t in longest.values())
+
+
 SCAN_BWD = [  # b, tiles' worth of tokens and a few more, ch, G, N, io, wide rows, tiles a segment
     (890, 4, 8, 1, 4, BF, True, 4),
     (600, 4, 5, 1, 4, F32, False, 2),
@@ -103,9 +113,15 @@ def test_scan_bwd_plan(case):
     m, nseg, size = bwd_plan(b, T, ch, G, N)
     assert m == want and nseg >= 2
     d = m3.SelDims(b, ch, G, N, m3.io_dtype_of(io))
-    assert m3.m3_sel_bwd_workspace_bytes(d, T) == size
-    # and no other number of tiles a segment would have this size
+    assert m3.m3_sel_bwd_workspace_bytes(d, T) == bwd_serves(b, T, ch, G, N) >= size
+    # no other number of tiles a segment would have this size: the call refuses less (here) and
+    # takes as much (on the GPU)
     assert all(size != bwd_plan(b, T, ch, G, N, k)[2] for k in (1, 2, 4) if k != m)
+    P, rows = 0x10000, lambda w: m3.m3_rows(0x10000, T * w, w)
+    inputs = bytes(m3.m3_sel_inputs(*[rows(w) for w in (ch, ch, G * N, G * N, ch)], P, P, P, 0))
+    grads = bytes(m3.m3_sel_grads(*[rows(w) for w in (ch, ch, G * N, G * N, ch)], P, P, P, P))
+    assert m3.load_library().m3_sel_bwd(bytes(d.c()), T, inputs, P, bytes(rows(ch)), P, grads, P,
+                                        size - 1, 0, None) == m3.M3_ERR_WORKSPACE
 
 
 @pytest.mark.gpu
@@ -156,13 +172,13 @@ FWD_SHAPE = {4: (64, 64), 8: (64, 64), 16: (32, 64), 24: (32, 32), 40: (32, 32),
 
 
 def fwd_plan(b, T, ch, G, N):
-    """Tiles (of 32 tokens) of a segment, segments, and the workspace's bytes."""
+    """Tiles (of 32 tokens) of a segment, segments, and the bytes that serve every length up to
+    T."""
     one, many = (b * G * -(-(ch // G) // CB) for CB in FWD_SHAPE[N])
     tiles = -(-T // 32)
     n = min(148 * 14 // many, tiles) if one <= 148 * 3 and tiles > 4 else 1
     per = -(-tiles // n)
-    n = -(-tiles // per)
-    return per, n, round256(4 * b * n * ch * (N + 1)) if n > 1 else 256
+    return per, -(-tiles // per), round256(4 * b * n * ch * (N + 1)) if n > 1 else 256
 
 
 SCAN_FWD = [  # b, T, ch, G, N, io, wide rows
@@ -216,14 +232,14 @@ def conv_run(b, T, C, slots):
 
 
 CONV = [  # b, T, C, W, io, options: wide rows with C a multiple of 16 bytes, else narrow ones
-    (590, 230, 64, 4, BF, "silu bias"),
-    (590, 230, 20, 4, F32, "silu bias"),
-    (590, 230, 21, 4, BF, "silu bias"),
-    (590, 230, 12, 3, F32, "bias"),
-    (590, 231, 16, 8, BF, "silu"),
-    (590, 233, 8, 8, F32, "silu bias"),
-    (590, 229, 9, 2, F32, "silu bias odd"),
-    (590, 232, 8, 1, BF, "silu bias"),
+    (290, 230, 64, 4, BF, "silu bias"),
+    (290, 230, 20, 4, F32, "silu bias"),
+    (290, 230, 21, 4, BF, "silu bias"),
+    (290, 230, 12, 3, F32, "bias"),
+    (290, 231, 16, 8, BF, "silu"),
+    (290, 233, 8, 8, F32, "silu bias"),
+    (290, 229, 9, 2, F32, "silu bias odd"),
+    (290, 232, 8, 1, BF, "silu bias"),
 ]
 
 
@@ -234,6 +250,8 @@ def test_conv_plan(case):
     assert conv_run(b, T, C, 148 * 7) >= 48
     s = conv_run(b, T, C, 148 * 4)
     assert s >= 48
+    # these fit one round of blocks, where the size that serves every length is that of the runs
+    assert b * -(-T // s) <= 148 * 4 and 148 * 4 // b == -(-T // s)
     assert m3.m3_conv_bwd_workspace_bytes(m3.ConvDims(b, C, W, m3.io_dtype_of(io)), T) == \
         round256(4 * b * -(-T // s) * (W + 1) * C)
 
@@ -294,6 +312,77 @@ def test_conv_bwd_long_runs(case):
         elif k != "dstate":      # a run's tokens, a warp's share of the runs, the warps
             tol = tol + (s + b * -(-T // s) / 8 + 32) * U32 * mag[k]
         tb.near(gr[k], want[k], tol, k)
+
+
+# ---------------------------------------------------------------- one workspace for several lengths
+
+def sizes(f, lengths):
+    out = [f(T) for T in lengths]
+    assert out == sorted(out)
+    return dict(zip(lengths, out))
+
+
+@pytest.mark.parametrize("b,ch,N", [(1, 2048, 16), (4, 4096, 16), (8, 1024, 24), (2, 64, 40),
+                                    (300, 4, 4), (37, 100, 200)])
+def test_a_workspace_serves_shorter_calls(b, ch, N):
+    """The size for a length is enough for every shorter one."""
+    d = m3.SelDims(b, ch, 1, N)
+    have = sizes(lambda T: m3.m3_sel_bwd_workspace_bytes(d, T), range(16, 6000, 16))
+    for T in range(16, 6000, 112):
+        assert have[T] == bwd_serves(b, T, ch, 1, N)
+    sizes(lambda T: m3.m3_sel_workspace_bytes(d, T), range(0, 20000, 32))
+    for W, io in ((4, m3.M3_BF16), (7, m3.M3_F32)):
+        d = m3.ConvDims(b, ch, W, io)
+        have, most = sizes(lambda T: m3.m3_conv_bwd_workspace_bytes(d, T), range(8, 20000, 8)), 0
+        for T in have:
+            most = max(most, -(-T // conv_run(b, T, ch, 148 * 4)))
+            assert have[T] == max(round256(4 * b * most * (W + 1) * ch), 256)
+        assert m3.m3_conv_bwd_workspace_bytes(d, 0) == 256
+
+
+@pytest.mark.gpu
+def test_conv_bwd_in_a_longer_calls_workspace():
+    b, C, W, T = 2, 64, 4, 2368              # one run more than half of 2376's would need
+    case = (b, T, C, W, F32, "silu bias")
+    x, w, bias, state, _, _ = tb.conv_inputs(case, 44)
+    dy = tb.rnd(torch.Generator().manual_seed(45), b, T, C)
+    d = m3.ConvDims(b, C, W, m3.M3_F32)
+    assert conv_run(b, T, C, 148 * 4) < conv_run(b, T + 8, C, 148 * 4)
+    out = []
+    for n in (T, T + 8):
+        gr = {k: tb.nan_like(v) for k, v in m3.alloc_conv_grads(d, T).items()}
+        m3.m3_conv_bwd(d, T, x, w, bias, state, dy, gr, m3.alloc_conv_bwd_workspace(d, n),
+                       flags=m3.M3_FLAG_SILU)
+        out.append(gr)
+    for k in out[0]:
+        assert torch.equal(out[0][k], out[1][k]), k
+
+
+@pytest.mark.gpu
+def test_scan_in_a_longer_calls_workspace():
+    """Forward in as many segments as with a workspace of its own (the same bits), backward."""
+    for b, T, longer, ch, G, call in ((100, 160, 192, 4, 4, "fwd"), (300, 320, 352, 64, 1, "bwd")):
+        c, _, sp = tb.scan_inputs((b, T, ch, G, 4, F32, "z D bias softplus"), 46)
+        d = m3.SelDims(b, ch, G, 4, m3.M3_F32)
+        short, long = (fwd_plan(b, n, ch, G, 4)[1] if call == "fwd" else bwd_plan(b, n, ch, G, 4)[2]
+                       for n in (T, longer))
+        assert short > long
+        out = []
+        for n in (T, longer):
+            h = c["h"].clone()
+            args = [c[k] for k in ("x", "dt", "A", "B", "C", "D", "z", "bias")]
+            if call == "fwd":
+                y = tb.nan_like(c["x"])
+                m3.m3_sel_fwd(d, T, *args, h, y, m3.alloc_sel_workspace(d, n),
+                              flags=m3.M3_FLAG_DT_SOFTPLUS)
+                out.append(dict(y=y, h=h))
+            else:
+                gr = {k: tb.nan_like(v) for k, v in m3.alloc_sel_grads(d, T).items()}
+                m3.m3_sel_bwd(d, T, *args, h, c["x"], None, gr, m3.alloc_sel_bwd_workspace(d, n),
+                              flags=m3.M3_FLAG_DT_SOFTPLUS)
+                out.append(gr)
+        for k in out[0]:
+            assert torch.equal(out[0][k], out[1][k]), (call, k)
 
 
 # ---------------------------------------------------------------- norm, backward
