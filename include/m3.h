@@ -506,10 +506,12 @@ m3_status m3_conv_bwd(const m3_conv_dims* dims, int32_t seqlen, const m3_rows* x
  *   B, C          m3_rows [batch][T][ngroups * dstate] io dtype
  *   A             [channels][dstate] fp32; D, dt_bias [channels] fp32 or NULL
  *   h             [batch][channels][dstate] fp32, updated in place (4-byte aligned)
- * dstate 1 to 256; ngroups divides channels.  The caller's contract is delta >= 0 and A <= 0
- * (a growing state is computed as it stands and may overflow).  An infinite or NaN input makes
- * its own channel's state and outputs infinite or NaN from its token on, and no other's (in B or
- * C: those of its group).  seqlen 0 does nothing.
+ * dstate 1 to 256; ngroups divides channels.  The caller's contract is delta >= 0 and A <= 0, A
+ * finite (a growing state is computed as it stands and may overflow).  An infinite or NaN x, dt or B
+ * makes the state and the outputs infinite or NaN from its token on, z and C the outputs of their
+ * token; x, dt and z those of their channel and no other, B and C those of their group.  With
+ * softplus a dt of -inf is a step of 0: the token leaves the state, and nothing becomes infinite.
+ * seqlen 0 does nothing.
  * Flags: M3_FLAG_DT_SOFTPLUS.
  * Workspace: m3_sel_workspace_bytes, 256-byte aligned.  Long sequences with too few channels to
  * fill the GPU are split into segments run side by side; the workspace holds each segment's

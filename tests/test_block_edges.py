@@ -144,3 +144,73 @@ def test_scan_step_after_softplus(call):
     tol = (1.33 * f64(dt).abs() + 12) * U32 * want
     tb.near(h.view(-1), want, tol, "delta")
     assert torch.equal(y.view(-1), h.view(-1))
+
+
+def minus_infinity(T, ch, N, seed):
+    """A prompt with softplus where some steps' dt is -inf, in 64 bits too, and an equal one with
+    -1000 there (whose softplus is 0 as well) for the bounds."""
+    c, _, sp = tb.scan_inputs((2, T, ch, 1, N, F32, "z D bias softplus"), seed)
+    r = {k: f64(v) for k, v in c.items()}
+    for t in (c["dt"], r["dt"]):
+        t[0, 3, 1], t[1, T - 1, 2], t[:, T // 2] = -1000.0, -1000.0, -1000.0
+    bound = ref.scan_bounds(T, N, ch, r["A"], torch.clamp(r["dt"], min=-20), r["bias"], True)
+    for t in (c["dt"], r["dt"]):
+        t[t == -1000.0] = float("-inf")
+    return c, r, bound
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [40, 200])
+def test_scan_step_of_minus_infinity(T):
+    """With softplus a dt of -inf is a step of zero: the token leaves the state, and nothing
+    becomes infinite or NaN, forward and backward."""
+    ch, N = 8, 16
+    c, r, rel = minus_infinity(T, ch, N, 52)
+    lens = [T, T]
+    y, h = tb.run_scan((2, T, ch, 1, N, F32, ""), c, None, True)
+    (want_y, want_h), (mag_y, mag_h) = (ref.scan(*r.values(), lens, True, absolute=a)
+                                        for a in (False, True))
+    tb.near(h, want_h, rel * mag_h + 1e-37, "h")
+    tb.near(y, want_y, half_step(F32) * want_y.abs() + (rel + 2.0 ** -20) * mag_y + 1e-37, "y")
+    g = torch.Generator().manual_seed(53)
+    dy, dhT = tb.rnd(g, 2, T, ch), tb.rnd(g, 2, ch, N)
+    want, mag = (ref.scan_bwd(*r.values(), lens, True, f64(dy), f64(dhT), absolute=a)
+                 for a in (False, True))
+    d = m3.SelDims(2, ch, 1, N, m3.M3_F32)
+    gr = {k: tb.nan_like(v) for k, v in m3.alloc_sel_grads(d, T).items()}
+    m3.m3_sel_bwd(d, T, c["x"], c["dt"], c["A"], c["B"], c["C"], c["D"], c["z"], c["bias"],
+                  c["h"], dy, dhT, gr, m3.alloc_sel_bwd_workspace(d, T),
+                  flags=m3.M3_FLAG_DT_SOFTPLUS)
+    for k, v in gr.items():
+        tol = (2 * rel + 2.0 ** -19 + U32 * (ch + 2 * T + 1)) * mag[k] + 1e-37
+        tb.near(v, want[k], tol, k)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,workspace", [(40, False), (300, True)])
+@pytest.mark.parametrize("name", ["x", "dt", "B", "z", "C"])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+def test_scan_where_an_infinity_goes(name, value, T, workspace):
+    """x, dt and B spoil the state and the outputs from their token on, z and C the outputs of
+    their token alone; x, dt and z those of their channel, B and C those of their group."""
+    case = (1, T, 12, 2, 16, F32, "z D bias softplus")
+    c, _, sp = tb.scan_inputs(case, 54)
+    base, h0 = tb.run_scan(case, c, None, sp, workspace)
+    at, per = 33, slice(6, 12) if name in ("B", "C") else slice(7, 8)
+    if name in ("B", "C"):
+        c[name][0, at, 1, 3] = value
+    else:
+        c[name][0, at, 7] = value
+    y, h = tb.run_scan(case, c, None, sp, workspace)
+    bad = torch.zeros_like(base, dtype=torch.bool)
+    bad[0, at:at + 1 if name in ("z", "C") else T, per] = True
+    assert not torch.isfinite(y[bad]).any()
+    assert torch.equal(y[~bad], base[~bad])
+    others = [i for i in range(12) if not per.start <= i < per.stop]
+    assert torch.equal(h[:, others], h0[:, others])
+    if name in ("z", "C"):
+        assert torch.equal(h, h0)
+    elif name == "B":
+        assert not torch.isfinite(h[0, per, 3]).any()
+    else:
+        assert not torch.isfinite(h[0, per]).any()
