@@ -6,9 +6,9 @@
 // thread k of a row holds the vectors k, k + TPR, .. of 8 neighbouring values, so the 128 values
 // of an e4m3 group lie in 16 neighbouring lanes.
 //
-// 32768 rows of 2048, bf16 in, fp32 residual, e4m3 out: 110 us (6.7 TB/s; the bytes take 113 at the
-// copy rate).  Backward of 16384 rows: 92 us (5.9 TB/s; 82): the next row's vectors on their way
-// while a row is summed brought it there from 132 us.
+// 32768 rows of 2048, bf16 in, fp32 residual, e4m3 out: 120 us, one call after another (6.2 TB/s; the
+// bytes take 113 at the copy rate).  Backward of 16384 rows: 96 us (5.6 TB/s; 82): the next row's
+// vectors on their way while a row is summed took 30 % off.
 #include <cuda_fp8.h>
 
 #include "block_internal.h"
@@ -62,34 +62,30 @@ __device__ __forceinline__ uint2 to_e4m3(const float (&q)[8]) {
     return out.v;
 }
 
-// Eight values of a row in e4m3, with the scale of their group of 128 (16 neighbouring lanes).
+// Eight values of a row in e4m3, with the scale of their group of 128 (16 neighbouring lanes): every
+// value the nearest step, ties to even.
 //
-// A value next to the middle of two steps lands on the other step for an error of one ulp.  The
-// reciprocal root is a factor of y and of max |y| alike, so the quotient is 448 r w / max |r w|;
-// with the products, the reciprocal of their largest and the quotient each rounded once, t is
-// within 2^-23 of it.  Where t (1 - 2^-22) and t (1 + 2^-22) go to the same step, so does the
-// quotient.  Else (one warp in six hundred) it is compared with g, the nearest value of five
-// significant bits (every step and every middle of two is one): the sign of 448 r w - g max |r w|
-// says on which side of g the quotient is rounded.  It is formed by FMA, the products' low parts
-// added where there are weights, exactly without them and to 2^-44 with them.
-// bf16 values without weights (SHORT) lie in the middle itself in most warps, else 2^-13 from it
-// (7 a and g b are integers below 2^13 for 8-bit a and b): one remainder step makes t the quotient
-// where that is representable, and the conversion does the rest (32768 rows of 2048: 74 us; 91
-// by the comparison).
-// So every value is the nearest step, ties to even; y / scale from rounded y and scale put 40 of 67
-// million on the other step, and took longer (122 us for 32768 rows of 2048 with an fp32 residual,
-// among others of their kind; now 118).
-template <bool WIDE, bool SHORT>
-__device__ __forceinline__ void store_e4m3(const float (&r)[8], const float (&w)[8], bool weighted, float mean,
+// A value next to the middle of two steps lands on the other step for an error of one ulp (y / scale
+// from rounded y and scale: 40 of 67 million).  The reciprocal root is a factor of y and of max |y|
+// alike, so the quotient is 448 r w / max |r w|; with the products, the reciprocal of their largest
+// and the quotient each rounded once, t is within 2^-23 of it.  Where t (1 - 2^-22) and t (1 + 2^-22)
+// go to the same step, so does the quotient.
+// Else the value is open, and the warp (one in six hundred) comes again with EXACT: it is compared
+// with g, the nearest value of five significant bits (every step and every middle of two is one).
+// The sign of 448 r w - g max |r w|, formed by FMA with the products' low parts (to 2^-44, exactly
+// where there are none), says on which side of g the quotient is rounded.
+// few_bits: r of 8 significant bits (bf16) and weights of 4 at most (none, or ones) give products
+// that lie in the middle itself in most warps, else 2^-17 from it (7 a and g b are integers below
+// 2^17 for 12-bit a and b): one remainder step makes t the quotient where that is representable,
+// and the conversion does the rest (32768 rows of 2048 without a residual: 70 us; 115 by the
+// comparison).
+template <bool EXACT, bool WIDE>
+__device__ __forceinline__ bool store_e4m3(const float (&r)[8], const float (&w)[8], bool few_bits, float mean,
                                            float rstd, uint8_t* o, int n, float* scale_out) {
     // rstd = ratio 2^e: the power of two keeps the products in range and rounds nothing
     const uint32_t bits = __float_as_uint(rstd);
     const float pow2 = __uint_as_float(bits & 0x7f800000u);
     const float ratio = __uint_as_float((bits & 0x007fffffu) | 0x3f800000u);
-    // what the reciprocal root lacks (one Newton step on mean rstd^2 = 1, by FMA), for the scale
-    const float p = mean * rstd, e = fmaf(mean, rstd, -p);
-    float low = 0.5f * ratio * (fmaf(-p, rstd, 1.f) - e * rstd);
-    if (!(fabsf(low) < ratio)) low = 0.f;      // a mean of 0, infinity or NaN has no remainder
     float hi[8], top = 0.f;
 #pragma unroll
     for (int j = 0; j < 8; j++) {
@@ -98,62 +94,63 @@ __device__ __forceinline__ void store_e4m3(const float (&r)[8], const float (&w)
     }
 #pragma unroll
     for (int s = 8; s > 0; s >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, s));
+    // what the reciprocal root lacks (one Newton step on mean rstd^2 = 1, by FMA), for the scale
+    const float p = mean * rstd, e = fmaf(mean, rstd, -p);
+    float low = 0.5f * ratio * (fmaf(-p, rstd, 1.f) - e * rstd);
+    if (!(fabsf(low) < ratio)) low = 0.f;      // a mean of 0, infinity or NaN has no remainder
     const float product = top * ratio;
     float amax = product + fmaf(top, low, fmaf(top, ratio, -product));
-    const bool tiny = amax < kAmaxFloor;
+    const bool tiny = amax < kAmaxFloor, finite = amax < __int_as_float(0x7f800000);
     float inv = tiny ? ratio * (kE4m3Max / kAmaxFloor) : kE4m3Max / top;
-    if (!(amax < __int_as_float(0x7f800000))) amax = inv = __int_as_float(0x7fffffff);   // infinite or NaN: all NaN
-    if (scale_out) *scale_out = max_nan(amax, kAmaxFloor) / kE4m3Max;
+    if (!finite) amax = inv = __int_as_float(0x7fffffff);
     union { uint8_t b[8]; uint2 v; } out;
+    bool open = false;
     float q[8];
-    if (SHORT && !weighted) {
-        const float back = tiny ? 0.f : inv * (1.f / kE4m3Max);
+    if constexpr (EXACT) {
+        float top_lo = -3.4e38f;      // the low part of the largest product
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            if (fabsf(hi[j]) == top) top_lo = fmaxf(top_lo, fmaf(fabsf(r[j] * pow2), fabsf(w[j]), -top));
+#pragma unroll
+        for (int s = 8; s > 0; s >>= 1) top_lo = fmaxf(top_lo, __shfl_xor_sync(0xffffffffu, top_lo, s));
+        if (tiny) {
+            top = kAmaxFloor / ratio;
+            top_lo = 0.f;
+        }
+        if (!finite) return false;
 #pragma unroll
         for (int j = 0; j < 8; j++) {
-            const float t = __fmul_rn(hi[j], inv);
-            q[j] = fmaf(fmaf(-t, top, kE4m3Max * hi[j]), back, t);
+            // 2^-9 on both sides keeps the products in range
+            const float h = fabsf(hi[j]);
+            const uint32_t g = (__float_as_uint(h * inv) + 0x40000u) & ~0x7ffffu;
+            const float step = __uint_as_float(g) * 0.001953125f, x = __fmul_rn(step, top);
+            const float gap = fmaf(0.875f, h, -x) - fmaf(step, top, -x) +
+                              fmaf(0.875f, fmaf(fabsf(r[j] * pow2), fabsf(w[j]), -h), -(step * top_lo));
+            q[j] = copysignf(__uint_as_float(gap > 0.f ? g + 1u : gap < 0.f ? g - 1u : g), hi[j]);
         }
         out.v = to_e4m3(q);
     } else {
-        constexpr float kSpread = 2.384185791015625e-07f;      // 2^-22
-        float above[8];
-#pragma unroll
-        for (int j = 0; j < 8; j++) {
-            const float t = __fmul_rn(hi[j], inv);
-            q[j] = t * (1.f - kSpread);
-            above[j] = t * (1.f + kSpread);
-        }
-        out.v = to_e4m3(q);
-        const uint2 other = to_e4m3(above);
-        const uint32_t apart[2] = {out.v.x ^ other.x, out.v.y ^ other.y};      // a byte a value
-        if (__any_sync(0xffffffffu, apart[0] | apart[1])) {
-            // the low part of the largest product
-            float top_lo = 0.f;
-            if (weighted && !__all_sync(0xffffffffu, tiny)) {
-                top_lo = -3.4e38f;
-#pragma unroll
-                for (int j = 0; j < 8; j++)
-                    if (fabsf(hi[j]) == top)
-                        top_lo = fmaxf(top_lo, fmaf(fabsf(r[j] * pow2), fabsf(w[j]), -fabsf(hi[j])));
-#pragma unroll
-                for (int s = 8; s > 0; s >>= 1) top_lo = fmaxf(top_lo, __shfl_xor_sync(0xffffffffu, top_lo, s));
-            }
-            if (tiny) {
-                top = kAmaxFloor / ratio;
-                top_lo = 0.f;
-            }
+        if (scale_out) *scale_out = max_nan(amax, kAmaxFloor) / kE4m3Max;
+        if (few_bits) {
+            const float back = tiny ? 0.f : inv * (1.f / kE4m3Max);
 #pragma unroll
             for (int j = 0; j < 8; j++) {
-                if (!(apart[j / 4] & (0xffu << (j % 4 * 8)))) continue;
-                // 2^-9 on both sides keeps the products in range
-                const float h = fabsf(hi[j]);
-                const uint32_t g = (__float_as_uint(h * inv) + 0x40000u) & ~0x7ffffu;
-                const float step = __uint_as_float(g) * 0.001953125f, x = __fmul_rn(step, top);
-                float gap = fmaf(0.875f, h, -x) - fmaf(step, top, -x);
-                if (weighted) gap += fmaf(0.875f, fmaf(fabsf(r[j] * pow2), fabsf(w[j]), -h), -(step * top_lo));
-                const float side = __uint_as_float(gap > 0.f ? g + 1u : gap < 0.f ? g - 1u : g);
-                out.b[j] = __nv_cvt_float_to_fp8(copysignf(side, hi[j]), __NV_SATFINITE, __NV_E4M3);
+                const float t = __fmul_rn(hi[j], inv);
+                q[j] = fmaf(fmaf(-t, top, kE4m3Max * hi[j]), back, t);
             }
+            out.v = to_e4m3(q);
+        } else {
+            constexpr float kSpread = 2.384185791015625e-07f;      // 2^-22
+            float above[8];
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const float t = __fmul_rn(hi[j], inv);
+                q[j] = t * (1.f - kSpread);
+                above[j] = t * (1.f + kSpread);
+            }
+            out.v = to_e4m3(q);
+            const uint2 other = to_e4m3(above);
+            open = out.v.x != other.x || out.v.y != other.y;
         }
     }
     if constexpr (WIDE) {
@@ -163,10 +160,17 @@ __device__ __forceinline__ void store_e4m3(const float (&r)[8], const float (&w)
         for (int j = 0; j < 8; j++)
             if (j < n) o[j] = out.b[j];
     }
+    return open;
 }
 
+// Rows of up to 16384 values in e4m3: 1152 threads an SM, 56 registers (32768 rows of 2048, bf16 without
+// a residual: 73 us; 77 with the 64 that it takes by itself, and at 48 they spill).
+template <int OUT, int NV, int THREADS>
+constexpr int fwd_blocks = OUT == M3_OUT_E4M3 && NV == 2 ? 1152 / THREADS : 1;
+
 template <typename IO, typename RES, int OUT, int TPR, int NV, bool WIDE>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_fwd_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, fwd_blocks<OUT, NV, TPR < 128 ? 128 : TPR>)
+norm_fwd_kernel(const NormArgs a) {
     constexpr int RPB = TPR < 128 ? 128 / TPR : 1;
     __shared__ float sm[32];
     const int k = threadIdx.x % TPR;
@@ -192,17 +196,34 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_fwd_kernel(const N
     }
     row_sum<TPR>(ss, sm);
     const float mean = ss[0] / (float)a.d + a.eps, rstd = 1.f / sqrtf(mean);
+    bool open = false;
+    auto values = [&](auto exact, int v) {
+        const int i = (k + v * TPR) * 8, n = live ? min(max(a.d - i, 0), 8) : 0;
+        float w[8];
+#pragma unroll
+        for (int j = 0; j < 8; j++) w[j] = 1.f;
+        bool few_bits = sizeof(RES) == 2;
+        if (a.weight) {
+            Vec<float, 8>::load<WIDE>(w, a.weight + i, min(max(a.d - i, 0), 8));
+            if constexpr (sizeof(RES) == 2) {
+                uint32_t tail = 0;
+#pragma unroll
+                for (int j = 0; j < 8; j++) tail |= __float_as_uint(w[j]);
+                few_bits = !__any_sync(0xffffffffu, tail & 0xfffffu);
+            }
+        }
+        uint8_t* o = static_cast<uint8_t*>(a.y) + row * a.ys + i;
+        float* scale = n > 0 && i % 128 == 0 ? a.scales + row * ((a.d + 127) / 128) + i / 128 : nullptr;
+        open |= store_e4m3<decltype(exact)::value, WIDE>(r[v], w, few_bits, mean, rstd, o, n, scale);
+    };
 #pragma unroll
     for (int v = 0; v < NV; v++) {
         const int i = (k + v * TPR) * 8, n = live ? min(max(a.d - i, 0), 8) : 0;
         if (a.res_out)
             Vec<RES, 8>::template store<WIDE>(r[v], static_cast<RES*>(a.res_out) + row * a.ros + i, n);
-        float w[8];
-#pragma unroll
-        for (int j = 0; j < 8; j++) w[j] = 1.f;
-        if (a.weight) Vec<float, 8>::load<WIDE>(w, a.weight + i, min(max(a.d - i, 0), 8));
         if constexpr (OUT == M3_OUT_IO) {
-            float y[8];
+            float y[8], w[8];
+            if (a.weight) Vec<float, 8>::load<WIDE>(w, a.weight + i, min(max(a.d - i, 0), 8));
 #pragma unroll
             for (int j = 0; j < 8; j++) {
                 y[j] = r[v][j] * rstd;
@@ -210,10 +231,13 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_fwd_kernel(const N
             }
             Vec<IO, 8>::template store<WIDE>(y, static_cast<IO*>(a.y) + row * a.ys + i, n);
         } else {
-            uint8_t* o = static_cast<uint8_t*>(a.y) + row * a.ys + i;
-            float* scale = n > 0 && i % 128 == 0 ? a.scales + row * ((a.d + 127) / 128) + i / 128 : nullptr;
-            store_e4m3<WIDE, sizeof(RES) == 2>(r[v], w, a.weight != nullptr, mean, rstd, o, n, scale);
+            values(std::false_type{}, v);
         }
+    }
+    if constexpr (OUT == M3_OUT_E4M3) {
+        if (__any_sync(0xffffffffu, open))
+#pragma unroll
+            for (int v = 0; v < NV; v++) values(std::true_type{}, v);
     }
 }
 

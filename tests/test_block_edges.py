@@ -57,23 +57,29 @@ def test_norm_e4m3_values_are_the_nearest(weighted, d):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("weights", [None, [1.0], [0.5, 0.625, 0.75, 1.0, 1.25, 1.875], [1.0, 1.0625]])
 @pytest.mark.parametrize("residual", [False, True])
 @pytest.mark.parametrize("d", [2048, 1000])
-def test_norm_e4m3_of_short_values(d, residual):
-    """bf16 values without weights: about one in a hundred lies in the middle of two steps."""
+def test_norm_e4m3_of_short_values(d, residual, weights):
+    """bf16 values without weights, or with weights of few bits: about one in a hundred lies in the
+    middle of two steps.  Weights of four bits and of five, one more than the short way takes."""
     g = torch.Generator().manual_seed(56)
     x = torch.randn((64, d), generator=g).bfloat16()
     res = torch.randn((64, d), generator=g).bfloat16() if residual else None
     r = x if res is None else (x.float() + res.float()).bfloat16()
     n = -(-d // 128)
     pad = torch.zeros(64, n * 128, dtype=torch.float64)
-    pad[:, :d] = r.double().abs()
+    w = None if weights is None else torch.tensor(weights)[torch.randint(0, len(weights), (d,),
+                                                                         generator=g)]
+    p = r.double() if w is None else r.double() * w.double()
+    pad[:, :d] = p.abs()
     top = pad.view(64, n, 128).amax(-1)[:, torch.arange(d) // 128]
-    want, gap = nearest_e4m3(r.double(), top)
-    assert (gap == 0).sum() > 64 * d / 400
+    want, gap = nearest_e4m3(p, top)
+    assert (gap == 0).sum() > 64 * d / 1000
     dims = m3.NormDims(64, d, m3.M3_BF16, m3.M3_BF16, m3.M3_OUT_E4M3)
     q = torch.empty(64, d, dtype=torch.float8_e4m3fn, device="cuda")
-    m3.m3_norm_fwd(dims, x.cuda(), None if res is None else res.cuda(), None, 1e-6, q,
+    m3.m3_norm_fwd(dims, x.cuda(), None if res is None else res.cuda(),
+                   None if w is None else w.cuda(), 1e-6, q,
                    m3.alloc_norm_scales(dims))
     assert torch.equal(f64(q.float()), want)
 
