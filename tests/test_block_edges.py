@@ -23,14 +23,11 @@ def nearest_e4m3(p, m):
     return torch.copysign((k + up) * unit, p), gap.abs() / (448 * p.abs() + 1e-300)
 
 
-@pytest.mark.gpu
-@pytest.mark.parametrize("d", [2048, 1000])
-@pytest.mark.parametrize("weighted", [True, False])
-def test_norm_e4m3_values_are_the_nearest(weighted, d):
-    """Values next to the middle of two e4m3 steps: each goes to the nearer one, and those in the
-    middle itself (without a weight there are some) to the even one."""
-    rows, n = 96, -(-d // 128)
-    g = torch.Generator().manual_seed(55)
+def near_middles(rows, d, weighted, seed):
+    """Rows and weights whose quotients lie next to the middle of two e4m3 steps, but for a group's
+    largest; the exact products and each value's largest."""
+    n = -(-d // 128)
+    g = torch.Generator().manual_seed(seed)
     x = 2 * torch.randn((rows, d), generator=g)
     w = 1 + 0.2 * torch.randn(d, generator=g) if weighted else torch.ones(d)
     p = x.double() * w.double()
@@ -46,7 +43,18 @@ def test_norm_e4m3_values_are_the_nearest(weighted, d):
         2.0 ** torch.randint(-9, 5, (rows, d), generator=g)
     near = (middle * top[:, at] / 448 / w.double()).float()
     x = torch.where(keep[:, :d], x, torch.copysign(near, x))
-    want, gap = nearest_e4m3(x.double() * w.double(), top[:, at])
+    return x, w, x.double() * w.double(), top[:, at]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [2048, 1000])
+@pytest.mark.parametrize("weighted", [True, False])
+def test_norm_e4m3_values_are_the_nearest(weighted, d):
+    """Values next to the middle of two e4m3 steps: each goes to the nearer one, and those in the
+    middle itself (without a weight there are some) to the even one."""
+    rows = 96
+    x, w, p, top = near_middles(rows, d, weighted, 55)
+    want, gap = nearest_e4m3(p, top)
     assert (gap < 2.0 ** -22).sum() > 0.9 * rows * d
     dims = m3.NormDims(rows, d, m3.M3_F32, m3.M3_F32, m3.M3_OUT_E4M3)
     q = torch.empty(rows, d, dtype=torch.float8_e4m3fn, device="cuda")
@@ -107,6 +115,46 @@ def test_norm_infinite_products_have_nan_scales(d):
     assert torch.isnan(sc[:, 1:3]).all() and torch.isnan(q[:, 128:384]).all()
     assert torch.equal(sc[:, [0, 3]], s0[:, [0, 3]])
     assert torch.equal(q[:, :128], q0[:, :128]) and torch.equal(q[:, 384:], q0[:, 384:])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [2048, 1000])
+def test_norm_e4m3_beside_a_spoiled_group(d):
+    """Open values of a warp whose other group is NaN, and the other way round."""
+    rows = 24
+    x, w, p, top = near_middles(rows, d, True, 57)
+    want, _ = nearest_e4m3(p, top)
+    w[300], w[700] = float("inf"), float("nan")
+    spoiled = torch.zeros(d, dtype=torch.bool)
+    spoiled[256:384] = spoiled[640:768] = True
+    dims = m3.NormDims(rows, d, m3.M3_F32, m3.M3_F32, m3.M3_OUT_E4M3)
+    q = torch.empty(rows, d, dtype=torch.float8_e4m3fn, device="cuda")
+    sc = m3.alloc_norm_scales(dims)
+    m3.m3_norm_fwd(dims, x.cuda(), None, w.cuda(), 1e-6, q, sc)
+    q = f64(q.float())
+    assert torch.equal(q[:, ~spoiled], want[:, ~spoiled]) and torch.isnan(q[:, spoiled]).all()
+    assert torch.isnan(sc[:, [2, 5]]).all() and torch.isnan(sc).sum() == 2 * rows
+
+
+@pytest.mark.gpu
+def test_norm_e4m3_below_the_floor():
+    """Groups whose largest y is next to 2^-100: above it their own scale, below it the floor's."""
+    rows, d = 16, 1024
+    g = torch.Generator().manual_seed(58)
+    x, w = torch.randn((rows, d), generator=g), 1 + torch.rand(d, generator=g)
+    for i, e in enumerate((-99, -101, -103, -106, -110, -120, -126)):
+        w[128 * i:128 * (i + 1)] *= 2.0 ** e
+    dims = m3.NormDims(rows, d, m3.M3_F32, m3.M3_F32, m3.M3_OUT_E4M3)
+    q = torch.empty(rows, d, dtype=torch.float8_e4m3fn, device="cuda")
+    sc = m3.alloc_norm_scales(dims)
+    m3.m3_norm_fwd(dims, x.cuda(), None, w.cuda(), 1e-6, q, sc)
+    y, _ = ref.norm(x.double(), None, w.double(), 1e-6, F32)
+    scale = y.view(rows, 8, 128).abs().amax(-1).clamp(min=2.0 ** -100) / 448
+    tb.near(sc, scale, (tb.rounds(d) + 4) * U32 * scale, "scales")
+    assert (scale[:, 0] > 2.0 ** -100 / 448).all() and (scale[:, 1:7] == 2.0 ** -100 / 448).sum() > 70
+    v = y / scale.repeat_interleave(128, 1)
+    # half a step of the value that is rounded, off by the roundings of the mean, the root and y
+    tb.near(q.float(), v, tb.e4m3_steps(v) * (1 + 2.0 ** -10) + tb.rounds(d) * U32 * v.abs(), "values")
 
 
 def test_binding_names_what_is_missing():
