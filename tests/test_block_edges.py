@@ -93,6 +93,25 @@ def test_norm_e4m3_of_short_values(d, residual, weights):
 
 
 @pytest.mark.gpu
+def test_norm_e4m3_of_short_values_and_huge_weights():
+    """Weights that are powers of two up to 2^126: 448 times a product is past fp32, y is not."""
+    g = torch.Generator().manual_seed(59)
+    x = torch.randn((16, 1024), generator=g).clamp(-1, 1).bfloat16()
+    w = 2.0 ** torch.tensor([0.0, 60, 100, 112, 116, 118, 122, 126]).repeat_interleave(128)
+    p = x.double() * w.double()
+    top = p.abs().view(16, 8, 128).amax(-1)
+    want, _ = nearest_e4m3(p, top.repeat_interleave(128, 1))
+    dims = m3.NormDims(16, 1024, m3.M3_BF16, m3.M3_BF16, m3.M3_OUT_E4M3)
+    q = torch.empty(16, 1024, dtype=torch.float8_e4m3fn, device="cuda")
+    sc = m3.alloc_norm_scales(dims)
+    m3.m3_norm_fwd(dims, x.cuda(), None, w.cuda(), 1e-6, q, sc)
+    scale = top / 448 / torch.sqrt(x.double().square().mean(1, keepdim=True) + 1e-6)
+    assert (scale < 2.0 ** 119).all()
+    tb.near(sc, scale, (tb.rounds(1024) + 4) * U32 * scale, "scales")
+    assert torch.equal(f64(q.float()), want)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("d", [512, 500])
 def test_norm_infinite_products_have_nan_scales(d):
     """An infinite weight, and a product of finite factors that overflows: the group holds an
