@@ -93,7 +93,10 @@ void conv_runs(const m3_conv_dims* d, int32_t T, int slots, int* seg, int* nseg)
         }
     }
 }
-constexpr int kConvFwdSlots = 148 * 7, kConvBwdSlots = 148 * 4;    // blocks an SM holds
+// Blocks that the GPU holds in bf16 with up to four taps.  fp32 holds six an SM forward (32 KiB of
+// shared memory each), and more taps four forward and two backward: their rounds are longer than
+// they are counted here.
+constexpr int kConvFwdSlots = 148 * 7, kConvBwdSlots = 148 * 4;
 
 // Bytes of the shares of `nseg` runs a sequence.
 size_t conv_bytes(const m3_conv_dims* d, int64_t nseg) {

@@ -59,7 +59,7 @@ struct SelArgs {
     int tile, ntile;       // backward: tokens per tile, tiles
     bool softplus;
     bool wide;             // rows of channels: 16-byte copies, pairs of channels in one access
-    bool wide_bc;          // the same of B and C (forward)
+    bool wide_bc;          // the same of B and C
     bool step_rows;
 };
 // Tokens of one staged tile: segments are multiples of it.

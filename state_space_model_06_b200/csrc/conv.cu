@@ -4,12 +4,13 @@
 // run of tokens; the W - 1 tokens before the current one stay in registers, so every x is read
 // once from memory but for the W - 1 tokens at the start of a run.
 //
-// Memory bounds it.  Prompt, 8 x 4096 tokens of 4096 channels, W 4, SiLU: 94 us (5.7 TB/s; 82 us at
-// the copy rate); the first forms took 299 us (eight channels and scalar arithmetic: 120 registers,
-// 16 warps an SM) and 164 (packed pairs).  Backward, 4 x 2048 tokens: 58 us where the bytes would
-// take 31: 124 registers hold 16 warps an SM, and each token's chain (convolution, logistic, three
-// sums) is not covered by four warps a sub-partition; five blocks an SM spill (98 us), and two
-// channels a thread, with 28 warps, double the copies and addresses (62 us).
+// Memory bounds it.  Prompt, 8 x 4096 tokens of 4096 channels, W 4, SiLU, bf16: 106 us, one call
+// after another (5.1 TB/s; 82 us at the copy rate), 94 alone in a graph; there the first forms took
+// 299 us (eight channels and scalar arithmetic: 120 registers, 16 warps an SM) and 164 (packed
+// pairs).  Backward, 4 x 2048 tokens: 62 us (58 alone) where the bytes would take 31: 124 registers
+// hold 16 warps an SM, and each token's chain (convolution, logistic, three sums) is not covered by
+// four warps a sub-partition; alone, five blocks an SM spill (98 us), and two channels a thread,
+// with 28 warps, double the copies and addresses (62 us).
 #include "block_internal.h"
 #include "block_common.cuh"
 
@@ -108,7 +109,7 @@ __device__ __forceinline__ void load_window(const ConvArgs& a, const IO* x, long
 // A thread's coming tokens: R tensors, groups of U tokens, D groups on their way.  With wide rows
 // they come by asynchronous copies into places that the thread alone reads, so there is nothing
 // to wait for but its own copies; loads into registers held up to 3.5 TB/s (the prompt case:
-// 152 us), as a thread's registers hold only a few tokens and its loads share few scoreboards.
+// 152 us alone), as a thread's registers hold only a few tokens and its loads share few scoreboards.
 template <typename IO, int R, int D, bool WIDE>
 struct Ahead {
     static constexpr int U = 4;

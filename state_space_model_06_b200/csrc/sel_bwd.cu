@@ -23,7 +23,7 @@
 // other instructions).
 //
 // Three passes over the exponentials (one in step 1, two in step 3) take 0.36 ms of the exponential
-// unit at 4 x 2048 tokens of 4096 channels of 16 states; it takes 1.18 ms in all (step 1 0.27, the
+// unit at 4 x 2048 tokens of 4096 channels of 16 states; it takes 1.19 ms in all (step 1 0.27, the
 // chain 0.03, step 3 0.87, the sums 0.03).  Step 3 is short of issue slots and of warps to fill
 // them: 532 instructions for 32 channel-tokens, of which a third is the walk itself, at 54 % of the
 // slots with 12 warps an SM (168 registers; at 128 the spills cost 40 %, and
@@ -43,8 +43,11 @@ struct BwdShape : SelShape<NT_, S_, WARPS_, L_> {
     using Base::NT; using Base::WARPS; using Base::L; using Base::PB; using Base::CB;
     using Base::NP; using Base::THREADS;
     static constexpr int K = K_;                 // tokens of a piece
-    static constexpr int MIN_BLOCKS = NT * K <= 16 ? 384 / THREADS : 1;   // 168 registers a thread
-    static constexpr int LOCAL_BLOCKS = NT == 4 ? 640 / THREADS : 1;      // 102 registers
+    // 168 registers a thread leave room for 12 warps an SM.  Shared memory admits as many in bf16 from
+    // 5 to 64 states and in fp32 from 5 to 8; else 8 (fp32: 6) up to 4 states, 8 in fp32 from 9 on,
+    // and above 64 states 8, above 128 four, where the limit brings no warp.
+    static constexpr int MIN_BLOCKS = NT * K <= 16 ? 384 / THREADS : 1;
+    static constexpr int LOCAL_BLOCKS = NT == 4 ? 640 / THREADS : 1;      // 96 registers, 20 warps
     // shared memory, in floats
     static constexpr int O_BC = 0;                              // [L][2][NP]
     static constexpr int O_DD = O_BC + L * 2 * NP;              // [L][PB] float4: delta, delta x of two channels
@@ -645,7 +648,7 @@ cudaError_t bwd_t(const SelArgs& a, cudaStream_t s) {
 }
 
 // The lane shape by the number of states.  At 16 states (4 x 2048 tokens of 4096 channels) four a lane
-// take 1.18 ms; two a lane, with 16 warps an SM instead of 12, take 1.47 (more lanes to sum over), and
+// take 1.19 ms; two a lane, with 16 warps an SM instead of 12, take 1.47 (more lanes to sum over), and
 // blocks of two warps 1.29; at 64, eight a lane take half as long again (registers spill).
 template <typename F>
 cudaError_t by_n(int N, F f) {

@@ -8,7 +8,7 @@
 // its own, so the chunked matrix form of the mixer's scan does not apply: the work is one ex2 and
 // four fp32 operations a cell on registers.  The exponential unit (16 a clock and SM) bounds it:
 // 8 x 2048 tokens of 4096 channels of 16 states need 1.34e9 of them with softplus and gate, 298 us,
-// where the memory would take 83.  The prompt kernel takes 500 us there (the unit 58 % busy, issue
+// where the memory would take 83.  The prompt kernel takes 503 us there (the unit 58 % busy, issue
 // slots 68 %, shared memory 69 %): 189 instructions for 32 channel-tokens of 16 states, of which the
 // recurrence itself is half; the rest is the step and the gate (49), the sum over the lanes of a
 // channel (28) and the staging.  What was measured and not kept: two, four or eight tokens' decays
@@ -307,8 +307,8 @@ __global__ void __launch_bounds__(128) sel_step_kernel(const SelArgs a) {
 // One token for N = 4 SL up to 32 and rows on 16 bytes: SL lanes share a channel, four states
 // each.  A warp takes 32 channels of one sequence: each lane loads and prepares one channel's x, dt
 // and z; then SL turns go over 32 / SL channels each, whose states are one contiguous stretch of
-// memory.  The state's bytes bound it: 23.2 us at 256 sequences of 4096 channels of 16 states (6.2
-// TB/s).  Warps that keep A over 2, 4, 8 sequences take 30, 28, 28 us: they need twice the
+// memory.  The state's bytes bound it: 26 us at 256 sequences of 4096 channels of 16 states, one call
+// after another (5.5 TB/s), 23 alone in a graph.  There, warps that keep A over 2, 4, 8 sequences take 30, 28, 28 us: they need twice the
 // registers, and half as many fit an SM.  Everything is asked for before anything is used: with D
 // loaded where it is needed, behind the sums, it takes 27 us.
 template <typename IO, int SL>
@@ -399,8 +399,8 @@ cudaError_t fwd_t(const SelArgs& a, cudaStream_t s) {
 
 // The lane shape of a forward call, by the number of states.  For up to 16 states: with the whole
 // sequence in one piece the channels alone make the warps, so a lane holds two states (8 x 2048
-// tokens of 4096 channels: 494 us, 540 with four); segments bring as many warps as one likes, and
-// four states a lane take fewer instructions (16384 tokens of 2048 channels: 396 us, 436 with two).
+// tokens of 4096 channels: four a lane take 9 % longer); segments bring as many warps as one likes, and
+// four states a lane take fewer instructions (16384 tokens of 2048 channels: two a lane take 10 % longer).
 template <typename F>
 auto fwd_shape(int N, bool segments, F f) {
     if (N <= 4) return f(SelShape<2, 2, 2, 32>{});
@@ -444,8 +444,9 @@ cudaError_t step_t(const SelArgs& a, cudaStream_t s) {
 // Segments.  A segmented call computes every decay twice (measured 1.75 times the work) and takes
 // three launches instead of one, so it pays for more than about 128 tokens where the blocks of one
 // pass would leave more than half of the GPU idle: then as many segments as fill it about twice (14
-// blocks an SM: 378 us for 16384 tokens of 2048 channels, 397 with 8), down to one tile of tokens
-// each (3 x 509 tokens of 1001 channels: 37 us, 39 with two tiles at least).
+// blocks an SM: 391 us for 16384 tokens of 2048 channels, one call after another; 8 take 5 % longer),
+// down to one tile of tokens each (3 x 509 tokens of 1001 channels, alone in a graph: 37 us, 39 with
+// two tiles at least; 47 to 49 among other calls).
 static int sel_fwd_most_segments(int batch, int T, int D, int G, int N) {
     auto blocks = [&](bool segments) {
         const int CB = fwd_shape(N, segments, [](auto sh) { return decltype(sh)::CB; });
