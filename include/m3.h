@@ -592,6 +592,9 @@ m3_status m3_sel_bwd(const m3_sel_dims* dims, int32_t seqlen, const m3_sel_input
  *            y stands for q * scale.  A group that holds a NaN or an infinity has a NaN scale.
  * Strides are in elements and at least width.  width is at most 32768.  eps >= 0
  * (M3_ERR_SHAPE otherwise).  rows 0 does nothing.  No workspace.
+ * The squares are summed in fp32, forward and backward: the caller's contract is values whose sum
+ * of squares fp32 holds (above it y and the gradients are 0, and with eps 0 a row whose squares
+ * all vanish has infinite or NaN y).
  */
 typedef enum { M3_OUT_IO = 0, M3_OUT_E4M3 = 1 } m3_norm_out;
 

@@ -80,16 +80,19 @@ m3_status conv_dims_ok(const m3_conv_dims* d) {
 // tokens read again at its start), and `slots` blocks run at a time: of 8, 16, .. 128 tokens the
 // run that takes the least time in whole rounds of blocks.  At least 8, so that only the first run
 // reaches back into the state.
+int64_t conv_columns(const m3_conv_dims* d) { return (int64_t)d->batch * ((d->channels + 511) / 512); }
+int64_t conv_cost(int64_t columns, int64_t T, int s, int slots) {
+    return (columns * ((T + s - 1) / s) + slots - 1) / slots * (s + 8);
+}
 void conv_runs(const m3_conv_dims* d, int32_t T, int slots, int* seg, int* nseg) {
-    const int64_t columns = (int64_t)d->batch * ((d->channels + 511) / 512);
+    const int64_t columns = conv_columns(d);
     int64_t best = 0;
     for (int s = 8; s <= 128; s += 8) {
-        const int64_t n = ((int64_t)T + s - 1) / s;
-        const int64_t cost = (columns * n + slots - 1) / slots * (s + 8);
+        const int64_t cost = conv_cost(columns, T, s, slots);
         if (s == 8 || cost < best) {
             best = cost;
             *seg = s;
-            *nseg = (int)n;
+            *nseg = (int)(((int64_t)T + s - 1) / s);
         }
     }
 }
@@ -103,20 +106,29 @@ size_t conv_bytes(const m3_conv_dims* d, int64_t nseg) {
     const size_t n = sizeof(float) * (size_t)d->batch * nseg * (d->width + 1) * d->channels;
     return n < 256 ? 256 : (n + 255) / 256 * 256;
 }
-// The most runs of any length up to T (the choice above does not grow with T).  Runs of s tokens
+// The most runs of any length up to T (the choice above goes up and down with T).  Runs of s tokens
 // make n of them where they are chosen at the longest such length, min(n s, T): the other choices
 // cost the most there.  They cannot be chosen where s + 8 for each s tokens cost more than runs of
 // 128 in their whole rounds: beyond 136 (1 + slots / columns) / (8 / s - 8 / 128) tokens.
 int64_t conv_most_runs(const m3_conv_dims* d, int32_t T, int slots) {
-    const double columns = (double)d->batch * ((d->channels + 511) / 512);
+    const int64_t columns = conv_columns(d);
+    auto chosen = [&](int s, int64_t t) {
+        const int64_t cost = conv_cost(columns, t, s, slots);
+        for (int k = 8; k <= 120; k += 8) {      // the nearest first: they cost least
+            if (s + k <= 128 && conv_cost(columns, t, s + k, slots) < cost) return false;
+            if (s - k >= 8 && conv_cost(columns, t, s - k, slots) <= cost) return false;
+        }
+        return true;
+    };
     int64_t best = ((int64_t)T + 127) / 128;
     for (int s = 8; s < 128; s += 8) {
-        const double end = 136. * (1. + slots / columns) / (8. / s - 0.0625) + s;
+        const double end = 136. * (1. + slots / (double)columns) / (8. / s - 0.0625) + s;
         int64_t n = ((end < T ? (int64_t)end : T) + s - 1) / s;
-        for (; n > best; n--) {
-            int seg, nseg;
-            conv_runs(d, n * s < T ? (int32_t)(n * s) : T, slots, &seg, &nseg);
-            if (seg == s) best = n;
+        while (n > best) {
+            if (chosen(s, n * s < T ? n * s : T))
+                best = n;
+            else      // nor are fewer runs of as many rounds, for which the others cost no more
+                n = ((columns * n + slots - 1) / slots - 1) * slots / columns;
         }
     }
     return best;
